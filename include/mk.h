@@ -245,6 +245,155 @@ const char* mk_status_str(mk_status s);
 mk_status mk_greedy_select(const float* logits, int batch, int vocab, int32_t* next_tokens,
                            int32_t* positions, void* stream);
 
+/* ------------------------------------------------------------------ beams
+ *
+ * Beam search over decode steps: mk_beam_select picks the continuations, mk_cache_reorder
+ * (or mk_qcache_reorder) lets the rows of the cache follow them. A sequence's beams are
+ * `beams` consecutive rows of the step's batch. */
+
+/* The n_out best continuations of each of `batch` sequences with `beams` rows of logits
+ * each: by total(k, v) = scores[k] + log_softmax(logits[k])[v], larger first; equal
+ * totals in the order of the beams, within a beam by the larger logit, equal logits by
+ * the lower token. Totals are formed and compared in 64 bits, from a row maximum and a
+ * 32-bit sum; scores are rounded to fp32 on the way out.
+ *   logits        device fp32 [batch * beams][vocab], rows row_stride elements apart
+ *                 (row_stride >= vocab; any 4-byte alignment, 16-byte rows are faster)
+ *   beams         1..16; n_out 1..32 and at most beams * vocab; vocab 1..2^24
+ *   scores        device fp32 [batch][beams], running log probabilities; a beam that
+ *                 is not in use has -infinity
+ *   finished      device int32 [batch][beams] or NULL. A nonzero beam's logits are not
+ *                 read: its one continuation is `eos` at its own score
+ *   eos           a token in [0, vocab) when `finished` is given; else unused
+ *   next_tokens   device int32 [batch][n_out], best first
+ *   parents       device int32 [batch][n_out]: the ROW (sequence * beams + beam) it continues
+ *   next_scores   device fp32 [batch][n_out]
+ *   next_finished device int32 [batch][n_out] or NULL (needs `finished`): 1 where the parent
+ *                 was finished or the token is eos, else 0
+ *   positions     device int32 [batch * beams] or NULL: each is incremented by one
+ * A masked logit (-infinity) and a NaN are chosen only where nothing else is left, with score
+ * -infinity; they add nothing to the row's sum. Infinite logits share their row's probability.
+ * next_scores may be scores, and next_finished may be finished (with n_out == beams); any other
+ * overlap of inputs and outputs is an error that is not detected.
+ * Enqueues one kernel launch (one cluster of CTAs per sequence) on the calling thread's current
+ * device, which must own the buffers and the stream; no synchronisation, no allocation, no
+ * workspace, capturable in a CUDA graph. MK_ERR_INVALID_ARG for a NULL required pointer, a size
+ * out of range or an eos outside [0, vocab); MK_ERR_UNSUPPORTED above the limits on beams,
+ * n_out, vocab and batch (2^20). */
+mk_status mk_beam_select(const float* logits, int64_t row_stride, int batch, int beams, int vocab, int n_out,
+                         const float* scores, const int32_t* finished, int32_t eos, int32_t* next_tokens,
+                         int32_t* parents, float* next_scores, int32_t* next_finished, int32_t* positions,
+                         void* stream);
+
+/* Rows of a KV cache take over other rows' slots, all at once and in place: for each row r < rows,
+ * layer and head, slots starts[r] <= s < lengths[parents[r]] of row r become those of row parents[r]
+ * as they were before the call. Reorders beams (parents from mk_beam_select, lengths = the advanced
+ * positions), forks a sequence into free rows, and compacts live rows over finished ones.
+ *   cfg              reads n_layers, n_kv_heads, head_dim, max_batch and max_seq only
+ *   k_cache, v_cache device bf16 [n_layers][max_batch][n_kv_heads][max_seq][head_dim], 16-byte aligned
+ *   rows             1..max_batch
+ *   parents          device int32 [rows]: a row below `rows`; the row itself or any other value
+ *                    leaves row r as it is
+ *   lengths          device int32 [rows]: the slots in use of each row BEFORE the call (clamped to
+ *                    [0, max_seq])
+ *   starts           device int32 [rows] or NULL (0): slots below starts[r] are the same in row r and
+ *                    its parent (a shared prompt) and are not moved
+ * Slots outside those ranges and rows >= rows are not touched. Enqueues one kernel launch on the
+ * calling thread's current device; no synchronisation, no allocation, capturable. MK_ERR_INVALID_ARG
+ * for a NULL pointer, an unaligned cache or a bad row count, MK_ERR_UNSUPPORTED for a geometry
+ * outside mk_create's ranges. */
+mk_status mk_cache_reorder(const mk_config* cfg, void* k_cache, void* v_cache, int rows, const int32_t* parents,
+                           const int32_t* lengths, const int32_t* starts, void* stream);
+
+/* ------------------------------------------------------------------ the 8-bit cache
+ *
+ * A KV cache in 8 bits with one scale per block of MK_QCACHE_BLOCK tokens of one head, for keys and
+ * for values: code = rint(x * (127 / amax)), scale = amax / 127, value = code * scale, amax the
+ * block's largest magnitude. It takes half the bytes of the bf16 cache, so half of what a decode step
+ * at a long context reads. The tokens of a row's open block (the last length % MK_QCACHE_BLOCK) stay
+ * bf16 in the tail buffers until the block is full, and are rounded once, from their own values.
+ * A row's length only grows, or goes back to a multiple of MK_QCACHE_BLOCK (its open block is then
+ * empty), or to a length inside the block that is open now.
+ * A block whose amax is below 2^-60 is held as zeros (scale 0). A block that holds an infinity or a
+ * NaN gets a NaN scale: whatever attends to it is NaN. */
+#define MK_QCACHE_BLOCK 32
+
+/* Caller-owned device buffers; nothing in them needs to be initialised. The codes and tails are
+ * 16-byte aligned. n_blocks = ceil(max_seq / MK_QCACHE_BLOCK). Accepted: 1..64 layers, max_batch 1..8,
+ * 1..32 KV heads, max_seq 1..2^20, head_dim 64 or 128. */
+typedef struct mk_qcache {
+    int32_t n_layers, max_batch, n_kv_heads, max_seq, head_dim, reserved0;
+    void* k_codes;   /* int8 [n_layers][max_batch][n_kv_heads][max_seq][head_dim] */
+    void* v_codes;
+    float* k_scale;  /* [n_layers][max_batch][n_kv_heads][n_blocks] */
+    float* v_scale;
+    void* k_tail;    /* bf16 [n_layers][max_batch][n_kv_heads][MK_QCACHE_BLOCK][head_dim] */
+    void* v_tail;
+} mk_qcache;
+
+/* Stores new keys and values: a decoded token, a prompt, or a bf16 cache that is taken over.
+ * Row r gets counts[r] tokens at slots positions[r] .. positions[r] + counts[r] - 1, in each of the
+ * layers first_layer .. first_layer + n_layers - 1; blocks that become full are quantised.
+ *   k_new, v_new  device bf16, 16-byte aligned; element (layer, row, head, token, dim) sits at
+ *                 layer * strides[0] + row * strides[1] + head * strides[2] + token * strides[3] + dim
+ *                 (layer counted from first_layer; strides in elements, multiples of 8, host array)
+ *   rows          1..max_batch; n_new >= 1: the tokens k_new and v_new hold per row
+ *   positions     device int32 [rows]: the row's length so far
+ *   counts        device int32 [rows] or NULL (n_new each)
+ * A row whose count is outside 1..n_new, or whose tokens would not fit [0, max_seq), is left as it is.
+ * k_new and v_new may not overlap the cache's buffers. One kernel launch; no allocation, capturable. */
+mk_status mk_qcache_append(const mk_qcache* c, int first_layer, int n_layers, int rows, int n_new, const void* k_new,
+                           const void* v_new, const int64_t* strides, const int32_t* positions, const int32_t* counts,
+                           void* stream);
+
+/* mk_cache_reorder on the 8-bit cache: closed blocks from the one that holds starts[r] move whole, the
+ * open block's tokens from starts[r] on. Row r's open block must have been that of its parent up to
+ * starts[r] (as it is where the slots below starts[r] are the same in both). */
+mk_status mk_qcache_reorder(const mk_qcache* c, int rows, const int32_t* parents, const int32_t* lengths,
+                            const int32_t* starts, void* stream);
+
+/* Decode attention of one layer over the 8-bit cache, one query token per row: for each row r and query
+ * head h, out = sum_s softmax_s(q . k_s / sqrt(head_dim)) v_s over the slots s = 0 .. positions[r] of
+ * KV head h / (n_heads / n_kv_heads).
+ *   n_heads       a multiple of n_kv_heads, at most 4 query heads per KV head (else MK_ERR_UNSUPPORTED)
+ *   max_ctx       positions[r] + 1 <= max_ctx <= max_seq; a larger position reads the first max_ctx
+ *                 slots, a negative one (an empty row) gives zeros
+ *   q, out        device fp32 [rows][n_heads][head_dim]
+ *   workspace     device, 16-byte aligned, mk_qcache_attention_workspace() bytes; need not be
+ *                 initialised, belongs to the call until it has run (calls that overlap on the GPU
+ *                 need one each); may be NULL where that is 0
+ * fp32 arithmetic to about 2^-22 of each product: the codes are exact in fp16 and the queries and
+ * weights enter the tensor cores as two fp16 parts. One or two kernel launches; no allocation,
+ * capturable; the same inputs give the same bits. */
+mk_status mk_qcache_attention(const mk_qcache* c, int layer, int rows, int n_heads, int max_ctx, const float* q,
+                              const int32_t* positions, float* out, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* Bytes of workspace a mk_qcache_attention call with these arguments needs (0 also for arguments it
+ * refuses). */
+size_t mk_qcache_attention_workspace(const mk_qcache* c, int rows, int n_heads, int max_ctx);
+
+/* One decode step on the 8-bit cache, as a sequence of ordinary kernels (one per op and layer,
+ * asynchronous on `stream`): mk_baseline_decode_step with the new key and value stored by
+ * mk_qcache_append and attention by mk_qcache_attention. For contexts beyond what
+ * mk_build_schedule takes, or a cache of half the bytes; it needs no schedule.
+ *   c                the cache; n_layers, n_kv_heads and head_dim as the handle's model
+ *   batch, max_ctx   1 <= batch <= c->max_batch; positions[b] + 1 <= max_ctx <= min(c->max_seq, the
+ *                    model's max_seq)
+ *   tokens, positions, logits  as for mk_decode_step; sequence b attends to slots 0..positions[b]
+ *   workspace        device, 256-byte aligned, mk_decode_step_qcache_workspace() bytes; need not be
+ *                    initialised, belongs to the call until it has run
+ *   status_out       device int32 or NULL: the step's device status (MK_OK, MK_ERR_BAD_TOKEN,
+ *                    MK_ERR_BAD_POSITION); it is not reported by mk_get_status
+ * A step with a bad token or position leaves the cache as it is and the logits unspecified. Runs on
+ * the calling thread's current device, which must be the handle's. No allocation, capturable. */
+mk_status mk_decode_step_qcache(mk_handle* h, const mk_qcache* c, int batch, int max_ctx, const int32_t* tokens,
+                                const int32_t* positions, float* logits, void* workspace, size_t workspace_bytes,
+                                int32_t* status_out, void* stream);
+
+/* Bytes of workspace a mk_decode_step_qcache call with these arguments needs (0 for arguments it
+ * refuses). */
+size_t mk_decode_step_qcache_workspace(mk_handle* h, const mk_qcache* c, int batch, int max_ctx);
+
 /* ------------------------------------------------------------------ inspection */
 
 /* One instruction of the per-SM lists (48 bytes). An SM's CTA runs its list in

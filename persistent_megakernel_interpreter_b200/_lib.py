@@ -53,9 +53,15 @@ class MkTmapSpec(ctypes.Structure):
                 ("dims", ctypes.c_uint64 * 5), ("strides", ctypes.c_uint64 * 4), ("box", ctypes.c_uint32 * 5)]
 
 
+class MkQcache(ctypes.Structure):
+    _fields_ = [(n, I32) for n in ("n_layers", "max_batch", "n_kv_heads", "max_seq", "head_dim", "reserved0")] + [
+        (n, P) for n in ("k_codes", "v_codes", "k_scale", "v_scale", "k_tail", "v_tail")]
+
+
 OP_QKV, OP_ATTN, OP_OPROJ, OP_GATEUP, OP_DOWN, OP_LMHEAD = 1, 2, 3, 4, 5, 6
 PROJ_AUTO, PROJ_CUDA_CORES, PROJ_TENSOR_CORES = 0, 1, 2
 NO_COUNTER = 0xFFFFFFFF
+QCACHE_BLOCK = 32
 
 STATUS = {0: "MK_OK", 1: "MK_ERR_INVALID_ARG", 2: "MK_ERR_CUDA", 3: "MK_ERR_UNSUPPORTED",
           4: "MK_ERR_NO_SCHEDULE", 5: "MK_ERR_TIMEOUT", 6: "MK_ERR_BAD_TOKEN",
@@ -111,10 +117,24 @@ def lib() -> ctypes.CDLL:
     L.mk_decode_steps_greedy.argtypes = [P, P, P, P, P, P, P, ctypes.c_int, P]
     L.mk_tensor_map_specs_host.argtypes = [ctypes.POINTER(MkConfig), ctypes.c_uint32, ctypes.POINTER(MkTmapSpec),
                                            ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)]
+    i = ctypes.c_int
+    L.mk_beam_select.argtypes = [P, ctypes.c_int64, i, i, i, i, P, P, I32, P, P, P, P, P, P]
+    L.mk_cache_reorder.argtypes = [ctypes.POINTER(MkConfig), P, P, i, P, P, P, P]
+    qc = ctypes.POINTER(MkQcache)
+    L.mk_qcache_append.argtypes = [qc, i, i, i, i, P, P, ctypes.POINTER(ctypes.c_int64), P, P, P]
+    L.mk_qcache_reorder.argtypes = [qc, i, P, P, P, P]
+    L.mk_qcache_attention.argtypes = [qc, i, i, i, i, P, P, P, P, ctypes.c_size_t, P]
+    L.mk_qcache_attention_workspace.argtypes = [qc, i, i, i]
+    L.mk_qcache_attention_workspace.restype = ctypes.c_size_t
+    L.mk_decode_step_qcache.argtypes = [P, qc, i, i, P, P, P, P, ctypes.c_size_t, P, P]
+    L.mk_decode_step_qcache_workspace.argtypes = [P, qc, i, i]
+    L.mk_decode_step_qcache_workspace.restype = ctypes.c_size_t
     for f in ("mk_create", "mk_build_schedule", "mk_decode_step", "mk_decode_steps_greedy", "mk_baseline_decode_step",
               "mk_decode_step_host", "mk_get_status", "mk_plan_schedule_host",
               "mk_get_schedule_info", "mk_read_counters", "mk_pack_weights_host", "mk_read_trace",
-              "mk_baseline_decode_step_noalloc", "mk_greedy_select", "mk_tensor_map_specs_host"):
+              "mk_baseline_decode_step_noalloc", "mk_greedy_select", "mk_tensor_map_specs_host",
+              "mk_beam_select", "mk_cache_reorder", "mk_qcache_append", "mk_qcache_reorder", "mk_qcache_attention",
+              "mk_decode_step_qcache"):
         getattr(L, f).restype = st
     _lib = L
     return L

@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "pack.h"
+#include "qcache.h"
 
 namespace mk {
 // megakernel.cu
@@ -22,6 +23,7 @@ size_t megakernel_smem_bytes(const Params& p);
 // baseline.cu
 cudaError_t baseline_launch(const Params& p, cudaStream_t stream, int n_sm);
 cudaError_t baseline_prepare(const Params& p);
+mk_status qcache_step_launch(const QcacheStep& s, cudaStream_t stream, int n_sm);
 
 // Device gather used by the packer: one warp per segment, 16-byte words.
 __global__ void k_gather(const Segment* segs, size_t n, uint8_t* dst) {
@@ -271,6 +273,24 @@ static mk_status make_tmaps(mk_handle* h, uint32_t stage_bytes) {
     return MK_OK;
 }
 
+// The part of the kernels' parameters that the handle and the step's size fix.
+static void shape_params(const mk_handle* h, int batch, int max_ctx, mk::Params* out) {
+    const mk_config& c = h->cfg;
+    const mk::Layout& L = h->lay;
+    mk::Params& p = *out;
+    p.L = L.L; p.H = L.H; p.nq = L.nq; p.nkv = L.nkv; p.d = L.d; p.F = L.F; p.V = L.V;
+    p.group = L.group; p.Q = L.Q; p.KVD = L.KVD;
+    p.B = batch; p.max_batch = c.max_batch; p.max_seq = c.max_seq; p.max_ctx = max_ctx;
+    p.eps = c.rms_eps;
+    p.packed = h->packed;
+    p.off_layer0 = L.off_layer0; p.layer_stride = L.layer_stride;
+    p.rel_qkv = L.rel_qkv; p.rel_o = L.rel_o; p.rel_gu = L.rel_gu; p.rel_down = L.rel_down;
+    p.off_norms = L.off_norms;
+    p.tile_h = L.tile_h; p.tile_o = L.tile_o; p.tile_f = L.tile_f;
+    p.rope_cos = h->rope;
+    p.rope_sin = h->rope + (size_t)c.max_seq * (L.d / 2);
+}
+
 static mk_status build_schedule_impl(mk_handle* h, int batch, int max_ctx, const mk_schedule_opts* opts) {
     if (!h) return MK_ERR_INVALID_ARG;
     const mk_config& c = h->cfg;
@@ -336,17 +356,7 @@ static mk_status build_schedule_impl(mk_handle* h, int batch, int max_ctx, const
 
     mk::Params& p = h->params;
     p = mk::Params{};
-    p.L = L.L; p.H = L.H; p.nq = L.nq; p.nkv = L.nkv; p.d = L.d; p.F = L.F; p.V = L.V;
-    p.group = L.group; p.Q = L.Q; p.KVD = L.KVD;
-    p.B = batch; p.max_batch = c.max_batch; p.max_seq = c.max_seq; p.max_ctx = max_ctx;
-    p.eps = c.rms_eps;
-    p.packed = h->packed;
-    p.off_layer0 = L.off_layer0; p.layer_stride = L.layer_stride;
-    p.rel_qkv = L.rel_qkv; p.rel_o = L.rel_o; p.rel_gu = L.rel_gu; p.rel_down = L.rel_down;
-    p.off_norms = L.off_norms;
-    p.tile_h = L.tile_h; p.tile_o = L.tile_o; p.tile_f = L.tile_f;
-    p.rope_cos = h->rope;
-    p.rope_sin = h->rope + (size_t)c.max_seq * (L.d / 2);
+    shape_params(h, batch, max_ctx, &p);
     p.x = reinterpret_cast<float*>(sb + o_x);
     p.q = reinterpret_cast<float*>(sb + o_q);
     p.attn = reinterpret_cast<float*>(sb + o_attn);
@@ -539,6 +549,74 @@ extern "C" mk_status mk_decode_step_host(mk_handle* h, const int32_t* tokens_hos
                                cudaMemcpyDeviceToHost, s));
     MK_CUDA(h, cudaStreamSynchronize(s));
     return MK_OK;
+}
+
+// The step's workspace: byte offsets, the attention's own last.
+struct QcacheWork {
+    size_t ctl, pos, x, q, attn, h, k, v, att, att_bytes, total;
+};
+
+static bool qcache_work(const mk_handle* h, const mk_qcache* c, int batch, int max_ctx, QcacheWork* w) {
+    if (!h || mk::qcache_check(c) != MK_OK) return false;
+    const mk::Layout& L = h->lay;
+    if (c->n_layers != L.L || c->n_kv_heads != L.nkv || c->head_dim != L.d) return false;
+    if (batch < 1 || batch > c->max_batch || max_ctx < 1 || max_ctx > c->max_seq || max_ctx > h->cfg.max_seq)
+        return false;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off = mk::align_up(off + bytes, 256);
+        return o;
+    };
+    const size_t B = (size_t)batch, kv = (size_t)L.L * B * L.nkv * L.d * sizeof(uint16_t);
+    w->ctl = take(sizeof(mk::Ctl));
+    w->pos = take(B * sizeof(int32_t));
+    w->x = take(B * L.H * sizeof(float));
+    w->q = take(B * L.Q * sizeof(float));
+    w->attn = take(B * L.Q * sizeof(float));
+    w->h = take(B * L.F * sizeof(float));
+    w->k = take(kv);
+    w->v = take(kv);
+    w->att_bytes = mk_qcache_attention_workspace(c, batch, L.nq, max_ctx);
+    w->att = take(w->att_bytes);
+    w->total = off;
+    return true;
+}
+
+extern "C" size_t mk_decode_step_qcache_workspace(mk_handle* h, const mk_qcache* c, int batch, int max_ctx) {
+    QcacheWork w;
+    return qcache_work(h, c, batch, max_ctx, &w) ? w.total : 0;
+}
+
+extern "C" mk_status mk_decode_step_qcache(mk_handle* h, const mk_qcache* c, int batch, int max_ctx,
+                                           const int32_t* tokens, const int32_t* positions, float* logits,
+                                           void* workspace, size_t workspace_bytes, int32_t* status_out,
+                                           void* stream) {
+    if (!h || !tokens || !positions || !logits || !workspace) return MK_ERR_INVALID_ARG;
+    QcacheWork w;
+    if (!qcache_work(h, c, batch, max_ctx, &w)) return MK_ERR_INVALID_ARG;
+    if (workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255)) return MK_ERR_INVALID_ARG;
+    if (const mk_status st = current_device_is(h); st != MK_OK) return st;
+    uint8_t* sb = static_cast<uint8_t*>(workspace);
+    mk::QcacheStep s{};
+    mk::Params& p = s.params;
+    shape_params(h, batch, max_ctx, &p);
+    p.ctl = reinterpret_cast<mk::Ctl*>(sb + w.ctl);
+    p.x = reinterpret_cast<float*>(sb + w.x);
+    p.q = reinterpret_cast<float*>(sb + w.q);
+    p.attn = reinterpret_cast<float*>(sb + w.attn);
+    p.hbuf = reinterpret_cast<float*>(sb + w.h);
+    p.kc = reinterpret_cast<uint16_t*>(sb + w.k);
+    p.vc = reinterpret_cast<uint16_t*>(sb + w.v);
+    p.tokens = tokens;
+    p.positions = positions;
+    p.logits = logits;
+    s.cache = c;
+    s.positions = reinterpret_cast<int32_t*>(sb + w.pos);
+    s.status_out = status_out;
+    s.attn_workspace = w.att_bytes ? sb + w.att : nullptr;
+    s.attn_workspace_bytes = w.att_bytes;
+    return mk::qcache_step_launch(s, static_cast<cudaStream_t>(stream), h->dev_sms);
 }
 
 extern "C" mk_status mk_get_status(mk_handle* h, mk_status* device_status, char* msg,

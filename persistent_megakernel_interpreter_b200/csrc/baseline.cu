@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 
 #include "mk_device.cuh"
+#include "qcache.h"
 
 namespace mk {
 
@@ -40,6 +41,22 @@ __global__ void k_validate(const __grid_constant__ Params p) {
     }
 }
 
+// The same checks for a step on the 8-bit cache, whose control block and status start
+// here. `ok` receives the positions the cache's kernels go by: a failed step's are -1 for
+// every row, which stores nothing.
+__global__ void k_validate_qcache(const __grid_constant__ Params p, int cache_seq, int32_t* ok, int32_t* status_out) {
+    if (threadIdx.x != 0) return;
+    uint32_t code = 0;
+    for (int b = 0; b < p.B && code == 0; ++b) {
+        const int tok = p.tokens[b], pos = p.positions[b];
+        if (tok < 0 || tok >= p.V) code = MK_ERR_BAD_TOKEN;
+        else if (pos < 0 || pos >= p.max_seq || pos >= cache_seq || pos >= p.max_ctx) code = MK_ERR_BAD_POSITION;
+    }
+    for (int b = 0; b < p.B; ++b) ok[b] = code ? -1 : p.positions[b];
+    p.ctl->status = code;
+    if (status_out) *status_out = (int32_t)code;
+}
+
 __device__ __forceinline__ const uint8_t* op_tiles(const Params& p, int op, int l) {
     const size_t lb = p.off_layer0 + (size_t)l * p.layer_stride;
     switch (op) {
@@ -53,7 +70,10 @@ __device__ __forceinline__ const uint8_t* op_tiles(const Params& p, int op, int 
 // One matvec op of one layer. The CTA first builds each sequence's input vector
 // in shared memory (RMSNorm where the op has one) with the same block routine as
 // the megakernel; then each warp takes tiles.
-template <int OP, int KC, int HD>
+//
+// STEP_KV: the new key and value go to slot 0 of a one-slot buffer (p.max_seq == 1)
+// instead of the cache slot of their position.
+template <int OP, int KC, int HD, bool STEP_KV = false>
 __global__ void __launch_bounds__(kBaseThreads) k_tiles(const __grid_constant__ Params p, int l,
                                                         uint32_t ntiles, uint32_t tile_bytes) {
     if (step_failed(p)) return;
@@ -96,6 +116,7 @@ __global__ void __launch_bounds__(kBaseThreads) k_tiles(const __grid_constant__ 
             dot4<KC, false>(base + (size_t)tl * tile_bytes, x, acc, lane, pol);
             RopeRow rr{nullptr, nullptr, 0};
             if constexpr (OP == MK_OP_QKV) rr = rope_row_global(p, b);
+            if constexpr (STEP_KV) rr.pos = 0;
             tile_epilogue<OP, HD>(p, l, b, tl, acc, lane, rr);
         }
     }
@@ -202,44 +223,86 @@ __global__ void __launch_bounds__(kBaseThreads) k_attn_merge(const __grid_consta
 
 // ------------------------------------------------------------------ host-side launch
 
-template <int KH, int KO, int KF, int HD>
-static cudaError_t launch_all(const Params& p, cudaStream_t st, int n_sm) {
+// CTAs of a matvec kernel over `units` tiles.
+static uint32_t matvec_blocks(uint32_t units, int n_sm) {
     const uint32_t warps_cap = (uint32_t)n_sm * 16;
-    auto blocks_for = [&](uint32_t units) {
-        const uint32_t w = units < warps_cap ? units : warps_cap;
-        return (w + kBaseWarps - 1) / kBaseWarps;
-    };
-    const size_t attn_smem = attn_item_smem<HD>(p.group, attn_kpad(p.part_keys));
+    const uint32_t w = units < warps_cap ? units : warps_cap;
+    return (w + kBaseWarps - 1) / kBaseWarps;
+}
+
+// A layer's ops behind its attention output.
+template <int KH, int KO, int KF, int HD>
+static void launch_after_attention(const Params& p, int l, cudaStream_t st, int n_sm) {
     const size_t in_h = (size_t)p.B * KH * 256 * 4 + 4 * kConsumerWarps;
     const size_t in_o = (size_t)p.B * KO * 256 * 4 + 4 * kConsumerWarps;
+    const uint32_t no = (uint32_t)p.H / 4;
+    k_tiles<MK_OP_OPROJ, KO, HD><<<matvec_blocks(no, n_sm), kBaseThreads, in_o, st>>>(p, l, no, p.tile_o);
+    const uint32_t ng = (uint32_t)p.F / 2;
+    k_tiles<MK_OP_GATEUP, KH, HD><<<matvec_blocks(ng, n_sm), kBaseThreads, in_h, st>>>(p, l, ng, p.tile_h);
+    k_down<KF><<<matvec_blocks((uint32_t)p.H / 4, n_sm), kBaseThreads, 0, st>>>(p, l);
+}
+
+template <int KH, int HD>
+static void launch_lm_head(const Params& p, cudaStream_t st, int n_sm) {
+    const size_t in_h = (size_t)p.B * KH * 256 * 4 + 4 * kConsumerWarps;
+    const uint32_t nl = (uint32_t)p.V / 4;
+    k_tiles<MK_OP_LMHEAD, KH, HD><<<matvec_blocks(nl, n_sm), kBaseThreads, in_h, st>>>(p, 0, nl, p.tile_h);
+}
+
+template <int KH, int KO, int KF, int HD>
+static cudaError_t launch_all(const Params& p, cudaStream_t st, int n_sm) {
+    const size_t attn_smem = attn_item_smem<HD>(p.group, attn_kpad(p.part_keys));
+    const size_t in_h = (size_t)p.B * KH * 256 * 4 + 4 * kConsumerWarps;
     k_validate<<<1, 32, 0, st>>>(p);
     const uint32_t tpg = (uint32_t)(p.group + 2) * (HD / 4);
     for (int l = 0; l < p.L; ++l) {
         const uint32_t nq = (uint32_t)p.nkv * tpg;
-        k_tiles<MK_OP_QKV, KH, HD><<<blocks_for(nq), kBaseThreads, in_h, st>>>(p, l, nq, p.tile_h);
+        k_tiles<MK_OP_QKV, KH, HD><<<matvec_blocks(nq, n_sm), kBaseThreads, in_h, st>>>(p, l, nq, p.tile_h);
         const uint32_t na = (uint32_t)(p.B * p.nkv * p.n_parts);
         k_attn_item<HD><<<na, kBaseThreads, attn_smem, st>>>(p, l);
         if (p.n_parts > 1) {
             const uint32_t nm = (uint32_t)(p.B * p.nq);
             k_attn_merge<HD><<<(nm + kBaseWarps - 1) / kBaseWarps, kBaseThreads, 0, st>>>(p);
         }
-        const uint32_t no = (uint32_t)p.H / 4;
-        k_tiles<MK_OP_OPROJ, KO, HD><<<blocks_for(no), kBaseThreads, in_o, st>>>(p, l, no, p.tile_o);
-        const uint32_t ng = (uint32_t)p.F / 2;
-        k_tiles<MK_OP_GATEUP, KH, HD><<<blocks_for(ng), kBaseThreads, in_h, st>>>(p, l, ng, p.tile_h);
-        k_down<KF><<<blocks_for((uint32_t)p.H / 4), kBaseThreads, 0, st>>>(p, l);
+        launch_after_attention<KH, KO, KF, HD>(p, l, st, n_sm);
     }
-    const uint32_t nl = (uint32_t)p.V / 4;
-    k_tiles<MK_OP_LMHEAD, KH, HD><<<blocks_for(nl), kBaseThreads, in_h, st>>>(p, 0, nl, p.tile_h);
+    launch_lm_head<KH, HD>(p, st, n_sm);
     return cudaGetLastError();
 }
 
-// Shared memory of the attention kernel for the current schedule (set once per
-// schedule, outside any stream capture).
+// The step on the 8-bit cache: the QKV kernel leaves the new key and value in a
+// one-slot buffer, the cache stores them (the block they fill is quantised), and its
+// attention reads the cache, the new token included.
+template <int KH, int KO, int KF, int HD>
+static mk_status launch_all_qcache(const QcacheStep& s, cudaStream_t st, int n_sm) {
+    Params p = s.params;
+    p.max_batch = p.B;
+    p.max_seq = 1;
+    const size_t in_h = (size_t)p.B * KH * 256 * 4 + 4 * kConsumerWarps;
+    const int64_t kv_row = (int64_t)p.nkv * p.d;
+    const int64_t strides[4] = {p.B * kv_row, kv_row, p.d, p.d};
+    k_validate_qcache<<<1, 32, 0, st>>>(s.params, s.cache->max_seq, s.positions, s.status_out);
+    const uint32_t nq = (uint32_t)p.nkv * (uint32_t)(p.group + 2) * (HD / 4);
+    for (int l = 0; l < p.L; ++l) {
+        k_tiles<MK_OP_QKV, KH, HD, true><<<matvec_blocks(nq, n_sm), kBaseThreads, in_h, st>>>(p, l, nq, p.tile_h);
+        const size_t at = (size_t)l * p.B * p.nkv * p.d;
+        mk_status r = mk_qcache_append(s.cache, l, 1, p.B, 1, p.kc + at, p.vc + at, strides, s.positions, nullptr, st);
+        if (r == MK_OK)
+            r = mk_qcache_attention(s.cache, l, p.B, p.nq, p.max_ctx, p.q, s.positions, p.attn, s.attn_workspace,
+                                    s.attn_workspace_bytes, st);
+        if (r != MK_OK) return r;
+        launch_after_attention<KH, KO, KF, HD>(p, l, st, n_sm);
+    }
+    launch_lm_head<KH, HD>(p, st, n_sm);
+    return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+}
+
+// Shared memory of the matvec kernels, for the largest batch: the limit belongs to the
+// kernel, not to a handle, so a smaller handle must not lower it under a larger one.
 template <int KH, int KO, int HD>
-static cudaError_t prepare_tiles(const Params& p) {
-    const int in_h = (int)((size_t)p.B * KH * 256 * 4 + 4 * kConsumerWarps);
-    const int in_o = (int)((size_t)p.B * KO * 256 * 4 + 4 * kConsumerWarps);
+static cudaError_t prepare_tiles() {
+    const int in_h = (int)((size_t)kMaxBatch * KH * 256 * 4 + 4 * kConsumerWarps);
+    const int in_o = (int)((size_t)kMaxBatch * KO * 256 * 4 + 4 * kConsumerWarps);
     cudaError_t e = cudaFuncSetAttribute(k_tiles<MK_OP_QKV, KH, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, in_h);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(k_tiles<MK_OP_GATEUP, KH, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, in_h);
@@ -247,15 +310,22 @@ static cudaError_t prepare_tiles(const Params& p) {
         e = cudaFuncSetAttribute(k_tiles<MK_OP_LMHEAD, KH, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, in_h);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(k_tiles<MK_OP_OPROJ, KO, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, in_o);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_tiles<MK_OP_QKV, KH, HD, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, in_h);
     return e;
 }
 
-cudaError_t baseline_prepare(const Params& p) {
+static cudaError_t prepare_matvecs(const Params& p) {
     const int KH = p.H / 256, KO = p.Q / 256;
-    cudaError_t e = cudaErrorInvalidValue;
-    if (KH == 2 && KO == 2 && p.d == 64) e = prepare_tiles<2, 2, 64>(p);
-    else if (KH == 8 && KO == 8 && p.d == 64) e = prepare_tiles<8, 8, 64>(p);
-    else if (KH == 12 && KO == 12 && p.d == 128) e = prepare_tiles<12, 12, 128>(p);
+    if (KH == 2 && KO == 2 && p.d == 64) return prepare_tiles<2, 2, 64>();
+    if (KH == 8 && KO == 8 && p.d == 64) return prepare_tiles<8, 8, 64>();
+    if (KH == 12 && KO == 12 && p.d == 128) return prepare_tiles<12, 12, 128>();
+    return cudaErrorInvalidValue;
+}
+
+// Once per schedule, outside any stream capture.
+cudaError_t baseline_prepare(const Params& p) {
+    const cudaError_t e = prepare_matvecs(p);
     if (e != cudaSuccess) return e;
     const int kpad = attn_kpad(p.part_keys);
     if (p.d == 64)
@@ -273,6 +343,16 @@ cudaError_t baseline_launch(const Params& p, cudaStream_t stream, int n_sm) {
     if (KH == 8 && KO == 8 && KF == 8 && p.d == 64) return launch_all<8, 8, 8, 64>(p, stream, n_sm);
     if (KH == 12 && KO == 12 && KF == 8 && p.d == 128) return launch_all<12, 12, 8, 128>(p, stream, n_sm);
     return cudaErrorInvalidValue;
+}
+
+mk_status qcache_step_launch(const QcacheStep& s, cudaStream_t stream, int n_sm) {
+    const Params& p = s.params;
+    if (prepare_matvecs(p) != cudaSuccess) return MK_ERR_CUDA;
+    const int KH = p.H / 256, KO = p.Q / 256, KF = p.F / 1024;
+    if (KH == 2 && KO == 2 && KF == 2 && p.d == 64) return launch_all_qcache<2, 2, 2, 64>(s, stream, n_sm);
+    if (KH == 8 && KO == 8 && KF == 8 && p.d == 64) return launch_all_qcache<8, 8, 8, 64>(s, stream, n_sm);
+    if (KH == 12 && KO == 12 && KF == 8 && p.d == 128) return launch_all_qcache<12, 12, 8, 128>(s, stream, n_sm);
+    return MK_ERR_UNSUPPORTED;
 }
 
 }  // namespace mk

@@ -3,9 +3,11 @@
 ``Megakernel(cfg, weights, max_batch, max_seq)`` packs device weights into a
 library handle; ``build_schedule``; ``decode_step`` (one persistent kernel
 launch), ``baseline_decode_step`` (the multi-kernel baseline) and
-``decode_step_host`` (host buffers in and out) run one step; ``greedy_select``
-picks the next tokens from a step's logits on the device. PyTorch supplies
-device memory and streams only.
+``decode_step_host`` (host buffers in and out) run one step, ``decode_step_qcache``
+one on an 8-bit cache (``qcache.QCache``); ``greedy_select`` and ``beam_select`` pick
+the next tokens from a step's logits on the device, ``cache_reorder`` lets the cache's
+rows follow the chosen beams, and ``decode_steps_beam`` runs the three in turn.
+PyTorch supplies device memory and streams only.
 """
 from __future__ import annotations
 
@@ -25,6 +27,12 @@ def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _here(*tensors) -> bool:
+    """Whether all of them are on the calling thread's current device, where the calls run."""
+    device = torch.cuda.current_device()
+    return all(t.is_cuda and t.get_device() == device for t in tensors)
 
 
 class Megakernel:
@@ -112,6 +120,75 @@ class Megakernel:
         self._step(_lib.lib().mk_baseline_decode_step, tokens, positions, k_cache, v_cache, logits,
                    stream)
 
+    def decode_step_qcache_workspace(self, cache, batch: int, max_ctx: int) -> torch.Tensor:
+        """A workspace for ``decode_step_qcache`` calls of this size. Calls that may overlap on the GPU
+        need one each."""
+        n = _lib.lib().mk_decode_step_qcache_workspace(self._h, cache._ref, batch, max_ctx)
+        if n == 0:
+            raise _lib.MkError(1, "mk_decode_step_qcache_workspace")
+        return torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", self.device))
+
+    def decode_step_qcache(self, tokens, positions, cache, logits, max_ctx: int | None = None, workspace=None,
+                           status=None, stream=None) -> None:
+        """One step as ordinary kernels on an 8-bit cache (``qcache.QCache``); it needs no schedule, and
+        contexts may be as long as the cache. ``status`` (int32 [1], optional) receives the step's
+        device status. Without a ``workspace`` one is allocated for the call."""
+        assert _here(tokens, positions, logits)
+        for t, dt in ((tokens, torch.int32), (positions, torch.int32), (logits, torch.float32)):
+            assert t.dtype == dt and t.is_contiguous()
+        batch = tokens.numel()
+        assert positions.numel() >= batch and logits.numel() >= batch * self.cfg.vocab
+        if status is not None:
+            assert _here(status) and status.dtype == torch.int32
+        max_ctx = min(cache.max_seq, self.max_seq) if max_ctx is None else max_ctx
+        if workspace is None:
+            with torch.cuda.stream(stream or torch.cuda.current_stream()):
+                workspace = self.decode_step_qcache_workspace(cache, batch, max_ctx)
+        assert _here(workspace) and workspace.is_contiguous()
+        _lib.check(_lib.lib().mk_decode_step_qcache(
+            self._h, cache._ref, batch, max_ctx, _ptr(tokens), _ptr(positions), _ptr(logits), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _ptr(status) if status is not None else None,
+            _stream(stream)), "mk_decode_step_qcache")
+
+    def decode_steps_beam(self, tokens, positions, cache, logits, scores, n_steps: int, finished=None, eos: int = -1,
+                          starts=None, generated=None, parents=None, max_ctx: int | None = None, workspace=None,
+                          stream=None) -> None:
+        """``n_steps`` beam-search steps with no host work between them. ``scores`` (fp32
+        [sequences][beams]) says how the batch's rows are grouped; each step decodes every row, picks
+        each sequence's best ``beams`` continuations (``beam_select``) into ``tokens``, ``scores`` and
+        ``finished``, advances the positions and lets the cache's rows follow. ``cache`` is a pair
+        (k_cache, v_cache) for ``decode_step``, or a ``qcache.QCache`` for ``decode_step_qcache`` (which
+        takes ``max_ctx`` and ``workspace``). ``starts`` (int32 [rows]): slots below are the same in
+        all beams of a sequence (the prompt). ``generated`` and ``parents`` (int32 [n_steps][rows],
+        optional) receive each step's tokens and the rows they continue."""
+        from .qcache import QCache
+        rows = tokens.numel()
+        assert scores.dim() == 2 and scores.numel() == rows
+        for t in (generated, parents):
+            assert t is None or (t.dtype == torch.int32 and t.is_contiguous() and t.numel() >= n_steps * rows)
+        s = stream or torch.cuda.current_stream()
+        with torch.cuda.stream(s):
+            came = torch.empty(rows, dtype=torch.int32, device=tokens.device) if parents is None else None
+            if isinstance(cache, QCache):
+                max_ctx = min(cache.max_seq, self.max_seq) if max_ctx is None else max_ctx
+                if workspace is None:
+                    workspace = self.decode_step_qcache_workspace(cache, rows, max_ctx)
+        for i in range(n_steps):
+            to = came if parents is None else parents.view(-1)[i * rows:(i + 1) * rows]
+            if isinstance(cache, QCache):
+                self.decode_step_qcache(tokens, positions, cache, logits, max_ctx=max_ctx, workspace=workspace, stream=s)
+            else:
+                self.decode_step(tokens, positions, cache[0], cache[1], logits, stream=s)
+            beam_select(logits.view(rows, -1), scores, tokens.view_as(scores), to.view_as(scores), scores,
+                        finished=finished, eos=eos, next_finished=finished, positions=positions, stream=s)
+            if isinstance(cache, QCache):
+                cache.reorder(to, positions, starts=starts, stream=s)
+            else:
+                cache_reorder(cache[0], cache[1], to, positions, starts=starts, stream=s)
+            if generated is not None:
+                with torch.cuda.stream(s):
+                    generated.view(-1)[i * rows:(i + 1) * rows].copy_(tokens.view(-1))
+
     def decode_step_host(self, tokens_host, positions_host, k_cache, v_cache, logits_host,
                          stream=None) -> None:
         """Host int32 tokens/positions in, host fp32 logits out (pinned memory preferred)."""
@@ -160,6 +237,57 @@ def greedy_select(logits: torch.Tensor, next_tokens: torch.Tensor, positions=Non
     _lib.check(_lib.lib().mk_greedy_select(_ptr(logits), logits.shape[0], logits.shape[1], _ptr(next_tokens),
                                            _ptr(positions) if positions is not None else None,
                                            _stream(stream)), "mk_greedy_select")
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, next_tokens: torch.Tensor, parents: torch.Tensor,
+                next_scores: torch.Tensor, finished=None, eos: int = -1, next_finished=None, positions=None,
+                stream=None) -> None:
+    """The best continuations of every sequence's beams, on the device and asynchronous on ``stream``.
+
+    ``logits`` fp32 [sequences * beams][vocab] (rows may be strided), ``scores`` fp32
+    [sequences][beams]; ``next_tokens`` and ``parents`` int32 and ``next_scores`` fp32
+    [sequences][n_out] receive, best first, the tokens, the rows they continue and score +
+    log_softmax(logits). A beam with a nonzero ``finished`` (int32 [sequences][beams]) goes on with
+    ``eos`` at its own score; ``next_finished`` receives who is finished then. ``positions``
+    (optional, one per row) are advanced by one. ``next_scores`` may be ``scores`` and
+    ``next_finished`` may be ``finished``."""
+    assert _here(logits, scores, next_tokens, parents, next_scores)
+    assert logits.dtype == torch.float32 and logits.dim() == 2 and (logits.stride(1) == 1 or logits.shape[1] == 1)
+    assert scores.dtype == torch.float32 and scores.dim() == 2 and scores.is_contiguous()
+    batch, beams = scores.shape
+    assert logits.shape[0] == batch * beams and next_tokens.dim() == 2
+    n_out = next_tokens.shape[1]
+    for t, dt in ((next_tokens, torch.int32), (parents, torch.int32), (next_scores, torch.float32)):
+        assert t.dtype == dt and t.shape == (batch, n_out) and t.is_contiguous()
+    for t, shape in ((finished, scores.shape), (next_finished, next_tokens.shape)):
+        assert t is None or (_here(t) and t.dtype == torch.int32 and t.shape == shape and t.is_contiguous())
+    if positions is not None:
+        assert _here(positions) and positions.dtype == torch.int32 and positions.numel() >= batch * beams
+        assert positions.is_contiguous()
+    stride = logits.stride(0) if logits.shape[0] > 1 else max(logits.stride(0), logits.shape[1])
+    _lib.check(_lib.lib().mk_beam_select(
+        _ptr(logits), stride, batch, beams, logits.shape[1], n_out, _ptr(scores),
+        _ptr(finished) if finished is not None else None, eos, _ptr(next_tokens), _ptr(parents), _ptr(next_scores),
+        _ptr(next_finished) if next_finished is not None else None,
+        _ptr(positions) if positions is not None else None, _stream(stream)), "mk_beam_select")
+
+
+def cache_reorder(k_cache: torch.Tensor, v_cache: torch.Tensor, parents: torch.Tensor, lengths: torch.Tensor,
+                  starts=None, stream=None) -> None:
+    """Row r of both caches (bf16 [layers][rows][heads][max_seq][dim]) takes over row parents[r]'s slots
+    starts[r] .. lengths[parents[r]] - 1, all rows at once and in place, asynchronous on ``stream``: beams
+    that follow ``beam_select``, a sequence forked into free rows, live rows moved over finished ones.
+    A parent that is the row itself or no row (-1) leaves the row as it is."""
+    from .qcache import _check_rows
+    assert _here(k_cache, v_cache) and k_cache.dtype == torch.bfloat16 and v_cache.dtype == torch.bfloat16
+    assert k_cache.dim() == 5 and v_cache.shape == k_cache.shape
+    assert k_cache.is_contiguous() and v_cache.is_contiguous()
+    rows = _check_rows(parents, lengths, starts)
+    n_layers, max_batch, heads, max_seq, dim = k_cache.shape
+    cfg = _lib.MkConfig(n_layers, 0, 0, heads, dim, 0, 0, 0.0, 0.0, max_batch, max_seq)
+    _lib.check(_lib.lib().mk_cache_reorder(ctypes.byref(cfg), _ptr(k_cache), _ptr(v_cache), rows, _ptr(parents),
+                                           _ptr(lengths), _ptr(starts) if starts is not None else None,
+                                           _stream(stream)), "mk_cache_reorder")
 
 
 def plan_schedule(cfg: ModelConfig, batch: int, max_ctx: int, n_sm: int, max_batch: int = 8,
