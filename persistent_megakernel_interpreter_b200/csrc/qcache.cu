@@ -6,7 +6,6 @@
 // tail buffers until the block is full, so a code is rounded once, from the token's
 // own bf16 value, and never again.
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -121,21 +120,36 @@ __global__ void __launch_bounds__(32 * kAppWarps) k_append(const __grid_constant
 // ------------------------------------------------------------------ attention
 //
 // out[h] = sum_i softmax_i(q[h] . k_i / sqrt(d)) v_i over slots i = 0 .. pos, for the
-// group's query heads h of one (row, KV head). Codes are whole numbers of at most 127
-// and so exact in fp16; the products run on the tensor cores (mma.sync m16n8k16,
-// fp32 accumulation) with the other operand split into two fp16 parts, 22 bits in
-// all: rows 0-7 of A hold the heads' high parts, rows 8-15 the low parts, and the two
-// rows of the accumulator are added.
-//   scores:  S[head][key]  = (sum_d q[head][d] code[key][d]) * k_scale
-//   outputs: O[head][d]   += sum_key w[head][key] code[key][d]
-// The value scale goes into the exponent: w = 2^(s + log2 v_scale - M), with M the
-// running maximum of that sum, and l += w / v_scale, so that O / l is the softmax's
-// output. The accumulator layout of S is the A layout of w, so the weights stay in
-// their lane.
+// group's query heads h of one (row, KV head).
+//
+// The codes are int8, so both products run on the tensor cores' integer path
+// (mma.sync m16n8k32, exact 32-bit sums) without a conversion of any code: the other
+// operand is cut into four 8-bit digits, which fill the 16 rows of A for 4 heads. Head
+// h has its digits 3 and 2 in rows h and h + 8, digits 1 and 0 in rows h + 4 and
+// h + 12, so lanes of groups g < 4 and g >= 4 hold two digits each of head g % 4.
+//   scores:  q as 30-bit whole numbers (its head's largest magnitude sets the step)
+//   outputs: weights as 32-bit whole numbers, 2^31 m 2^(s + e - M), where 2^e m is the
+//            block's value scale (1 <= m < 2) and M the running maximum of s + e; the
+//            softmax's sum is that of 2^(s + e - M) 2^-e.
+// Accumulators start at the bits of 1.5 * 2^23, so that read as a float they are that
+// plus the sum (below 2^22 in magnitude: 128 * 127 * 128 in a score, 255 * 127 * 64 in
+// an output), and one FMA turns each into its share of the fp32 result.
+//
+// A warp works alone on a batch of 8 KB (64 keys and values of 64 dims, 32 of 128), with
+// a running (M, l, O) of its own, fed by a private ring of asynchronous copies; the warps
+// join at the end.
 
 constexpr int kAttWarps = 4;
+// Batches in a warp's ring, and CTAs an SM holds. The 64-dim form needs about 180 registers a thread and
+// so runs two CTAs, with a batch more on the way each; at 128 dims three fit. 8 x 16384 keys of 64
+// dims: 23.8 us against 25.0 with (2, 3); 4 x 60001 of 128 dims: 56.4 us against 57.9 with (3, 2).
+__host__ __device__ constexpr int attn_stages(int hd) { return hd == 64 ? 3 : 2; }
+__host__ __device__ constexpr int attn_per_sm(int hd) { return hd == 64 ? 2 : 3; }
+constexpr int kHalf = 4096;            // bytes of a batch's keys, and of its values
+__host__ __device__ constexpr int batch_blocks(int hd) { return hd == 64 ? 2 : 1; }
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kWeightBits = 15.0f;   // weights are scaled by 2^15: at most 32768, fp16's normal range down to 2^-29
+constexpr uint32_t kMagicBits = 0x4b400000u;
+constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
 
 struct AttnArgs {
     const uint8_t* codes[2];
@@ -150,15 +164,17 @@ struct AttnArgs {
     int n_cta;                    // CTAs of the split over blocks (0: one CTA per (row, head), no partials)
 };
 
-__device__ __forceinline__ uint4 ld_code16(const uint8_t* p) {
-    uint4 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
-    return r;
+__device__ __forceinline__ uint32_t smem32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem32(dst)), "l"(src) : "memory");
 }
-__device__ __forceinline__ uint2 ld_code8(const uint8_t* p) {
-    uint2 r;
-    asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-    return r;
+__device__ __forceinline__ void copy4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -167,178 +183,284 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Bytes 0 and 2 of w (int8) as a pair of fp16: 0x6400 | (code + 128) is 1024 + code + 128.
-__device__ __forceinline__ uint32_t codes_even(uint32_t w) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, 0x00ff00ff, 0x64806480, 0x6a;" : "=r"(r) : "r"(w));
-    const __half2 h = __hsub2(*reinterpret_cast<__half2*>(&r), __half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t codes_odd(uint32_t w) { return codes_even(w >> 8); }
-
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+// C += A B, C read and written as 32-bit whole numbers; A's bytes signed (queries) or not (weights).
+__device__ __forceinline__ void mma_s8(uint32_t (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-
-// x, y as fp16 pairs: the high parts and what they leave.
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-    const __half2 h = __floats2half2_rn(x, y);
-    const float2 f = __half22float2(h);
-    const __half2 r = __floats2half2_rn(x - f.x, y - f.y);
-    hi = *reinterpret_cast<const uint32_t*>(&h);
-    lo = *reinterpret_cast<const uint32_t*>(&r);
+__device__ __forceinline__ void mma_u8(uint32_t (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// (the sum in accumulator c) * mul, exact for a power of two
+__device__ __forceinline__ float sum_of(uint32_t c, float mul) { return fmaf(__uint_as_float(c), mul, -kMagic * mul); }
 
-// A CTA's running result of one (row, KV head): per warp (and the tail) a maximum, a
-// sum and an output per head, joined at the end.
+// A CTA's running result of one (row, KV head): per warp (and the open block) a maximum, a
+// sum and an output per head, joined at the end; and each warp's ring of batches.
 template <int HD>
 struct AttnSmem {
-    float o[kAttWarps + 1][kMaxGroupHeads][HD];
+    static constexpr int kStages = attn_stages(HD);
+    alignas(16) uint8_t ring[kAttWarps][kStages][2][kHalf];
+    float scale[kAttWarps][kStages][2][2];   // keys' and values', of the batch's blocks
+    float tail_o[kMaxGroupHeads][HD];
     float m[kAttWarps + 1][kMaxGroupHeads];
     float l[kAttWarps + 1][kMaxGroupHeads];
     float q[kMaxGroupHeads][HD];
+    // Part p's output of head h: a warp's lies in its own ring once the ring is drained.
+    __device__ __forceinline__ float* o(int p, int h) {
+        return p == kAttWarps ? tail_o[h] : reinterpret_cast<float*>(ring[p]) + h * HD;
+    }
+};
+static_assert(kMaxGroupHeads * 128 * sizeof(float) <= 2 * kHalf, "a warp's outputs lie in its ring");
+
+// The 16-byte piece c of row r sits at piece swizzled(r, c) of its row, so that the
+// fragment reads below meet every bank once: of eight lanes that read a piece of keys in
+// one cycle, two rows come with the even or the odd pieces each; of the lanes that read
+// values, four rows two apart with two pieces each.
+template <int HD>
+__device__ __forceinline__ int swizzled(int r, int c) {
+    return HD == 64 ? c ^ (r >> 1 & 3) : c ^ (r & 7);
+}
+
+// The first `bytes` (2048 or 4096) of a batch's keys and values, and its scales.
+template <int HD>
+__device__ __forceinline__ void fetch_batch(AttnSmem<HD>& sm, int warp, int lane, int stage, const uint8_t* k, const uint8_t* v,
+                                            const float* ks, const float* vs, int blocks) {
+    constexpr int CPR = HD / 16, PER = kQBlock * HD / 512;   // pieces of a row; of a block, per lane
+#pragma unroll
+    for (int b = 0; b < batch_blocks(HD); ++b)
+        if (b < blocks) {
+#pragma unroll
+            for (int j = b * PER; j < (b + 1) * PER; ++j) {
+                const int i = j * 32 + lane, r = i / CPR, c = i % CPR;
+                const int at = r * HD + 16 * swizzled<HD>(r, c);
+                copy16(&sm.ring[warp][stage][0][at], k + i * 16);
+                copy16(&sm.ring[warp][stage][1][at], v + i * 16);
+            }
+        }
+    if (lane < 2 * blocks) copy4(&sm.scale[warp][stage][lane & 1][lane >> 1], (lane & 1 ? vs : ks) + (lane >> 1));
+}
+
+// The closed blocks [b0, b1) of one (row, KV head): where they lie, and a warp's fetches of them. Warp w
+// takes the batches at b0 + (w + 4 i) batch_blocks.
+template <int HD>
+struct AttnSource {
+    const uint8_t *k, *v;
+    const float *ks, *vs;
+    int b0, b1;
+    __device__ __forceinline__ AttnSource(const AttnArgs& a, size_t plane, int first, int last) : b0(first), b1(last) {
+        k = a.codes[0] + plane * a.max_seq * HD;
+        v = a.codes[1] + plane * a.max_seq * HD;
+        ks = a.scale[0] + plane * a.n_blocks;
+        vs = a.scale[1] + plane * a.n_blocks;
+    }
+    __device__ __forceinline__ int first(int warp) const { return b0 + warp * batch_blocks(HD); }
+    static constexpr int kStep = kAttWarps * batch_blocks(HD);
+    __device__ __forceinline__ void fetch(AttnSmem<HD>& sm, int warp, int lane, int blk, int stage) const {
+        if (blk < b1)
+            fetch_batch<HD>(sm, warp, lane, stage, k + (size_t)blk * (kQBlock * HD), v + (size_t)blk * (kQBlock * HD), ks + blk,
+                            vs + blk, min(batch_blocks(HD), b1 - blk));
+        copy_commit();
+    }
+    // The first batches, before anything else is done for these blocks.
+    __device__ __forceinline__ void start(AttnSmem<HD>& sm, int warp, int lane) const {
+#pragma unroll
+        for (int i = 0; i < attn_stages(HD) - 1; ++i) fetch(sm, warp, lane, first(warp) + i * kStep, i);
+    }
 };
 
-// Blocks [b0, b1) of one (row, KV head) by the CTA's warps, into sm.o/m/l[warp].
+// The blocks of src by the CTA's warps, into part `warp` of sm. src.start() has run.
 template <int HD>
-__device__ __forceinline__ void attn_blocks(const AttnArgs& a, AttnSmem<HD>& sm, size_t plane, int b0, int b1, int warp,
+__device__ __forceinline__ void attn_blocks(const AttnArgs& a, AttnSmem<HD>& sm, const AttnSource<HD>& src, int warp,
                                             int lane) {
-    constexpr int KS = 2048 / HD;            // keys of a step: 2 KB of keys, 2 KB of values
-    constexpr int NT = KS / 8;               // 8-key tiles
-    constexpr int C = HD / 64;               // 16-byte pieces of a key per lane
-    constexpr int VD = HD / 8;               // dims of a value per lane
-    const int g = lane >> 2, t = lane & 3;
-    // A fragments of q: head g's dims 64 c + 16 t + 4 i + {0, 2, 1, 3} in k-step 4 c + i. Each head
-    // is scaled by a power of two to magnitudes below 512, so both parts stay normal.
-    uint32_t qa[4 * C][4];
+    constexpr int BB = batch_blocks(HD), kStages = attn_stages(HD);
+    constexpr int KEYS = BB * kQBlock, NT = KEYS / 8;   // keys of a batch, 8-key tiles
+    constexpr int C = HD / 64;               // 16-byte pieces of a key per lane: C t, C t + 1, ..
+    constexpr int VD = HD / 8;               // dims of a value per lane: VD g, VD g + 1, ..
+    const int g = lane >> 2, t = lane & 3, head = g & 3;
+    const bool up = g >= 4;
+    // A of the scores: digits of q. K step j of a tile covers the lane's dims 16 (j / 2) + 8 (j % 2)
+    // + 0 .. 7 behind (HD / 4) t.
+    uint32_t qa[2 * C][4];
     float kmul;
     {
-        float v[C][16], big = 0.f;
+        float big = 0.f;
+        bool bad = false;
+        const float* q = sm.q[head < a.group ? head : 0] + t * (HD / 4);
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                v[c][e] = g < a.group ? sm.q[g < kMaxGroupHeads ? g : 0][64 * c + 16 * t + e] : 0.f;
-                big = fmaxf(big, fabsf(v[c][e]));
-            }
+        for (int e = 0; e < HD / 4; ++e) {
+            big = fmaxf(big, fabsf(q[e]));
+            bad |= !(fabsf(q[e]) <= 3.4e38f);
+        }
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        int ex = big > 0.f ? ilogbf(big) : 0;
-        ex = ex > 120 ? 120 : ex < -110 ? -110 : ex;
-        const float up = exp2f((float)(8 - ex));
-        kmul = exp2f((float)(ex - 8)) * kLog2e * rsqrtf((float)HD);
+        bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
+        bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
+        // |q| < 2^(ex + 1) becomes a whole number below 2^30, its digits within -128 .. 127
+        int ex = big > 0.f && !bad ? ilogbf(big) : 0;
+        ex = max(ex, -90);
+        const float step = exp2f((float)(29 - ex));
+        kmul = bad ? __int_as_float(0x7fffffff) : exp2f((float)(ex - 29)) * (HD == 64 ? 0.125f : 0.08838834764831845f) * kLog2e;
 #pragma unroll
-        for (int c = 0; c < C; ++c)
+        for (int j = 0; j < 2 * C; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float* w = &v[c][4 * i];
-                split2(w[0] * up, w[2] * up, qa[4 * c + i][0], qa[4 * c + i][1]);
-                split2(w[1] * up, w[3] * up, qa[4 * c + i][2], qa[4 * c + i][3]);
+            for (int w = 0; w < 2; ++w) {
+                uint32_t hi = 0, lo = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    int x = head < a.group ? __float2int_rn(q[16 * (j / 2) + 8 * (j % 2) + 4 * w + e] * step) : 0;
+                    int d[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        d[i] = (int)(signed char)(x & 255);
+                        x = (x - d[i]) >> 8;
+                    }
+                    hi |= (uint32_t)((up ? d[1] : d[3]) & 255) << (8 * e);
+                    lo |= (uint32_t)((up ? d[0] : d[2]) & 255) << (8 * e);
+                }
+                qa[j][2 * w] = hi;
+                qa[j][2 * w + 1] = lo;
             }
     }
-    float M = -1e30f, l = 0.f, o[VD][4];
-    float lv_ref = 0.f;
+    const float sm0 = up ? 256.0f : 16777216.0f, sm1 = up ? 1.0f : 65536.0f;       // a score's digits
+    const float vm0 = sm0 * 0x1p-31f, vm1 = sm1 * 0x1p-31f;                       // an output's
+    // a pair of weights (own, other half's) as bytes (lower digit, lower, upper, upper) in the keys' order
+    const uint32_t sel_w = up ? 0x1504u : 0x7362u;
+    // lanes of odd t read the two keys of a pair in the other order at 64 dims (other banks)
+    const bool odd = HD == 64 && (t & 1);
+    const uint32_t sel_lo = odd ? 0x1504u : 0x5140u, sel_hi = odd ? 0x3726u : 0x7362u;
+    float M = -1e30f, l = 0.f, o[VD][2];
+    int e_ref = 0;
 #pragma unroll
-    for (int i = 0; i < VD; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    const uint8_t* kc = a.codes[0] + plane * a.max_seq * HD;
-    const uint8_t* vc = a.codes[1] + plane * a.max_seq * HD;
-    const float* ksc = a.scale[0] + plane * a.n_blocks;
-    const float* vsc = a.scale[1] + plane * a.n_blocks;
-    constexpr int SPB = kQBlock / KS;        // steps per block
-    const int s1 = b1 * SPB;
-    for (int s = b0 * SPB + warp; s < s1; s += kAttWarps) {
-        const uint8_t* kp = kc + (size_t)s * 2048 + g * HD + 16 * t;
-        const uint8_t* vp = vc + (size_t)s * 2048 + (2 * t) * HD + g * VD;
-        uint4 kr[NT][C];
+    for (int i = 0; i < VD; ++i) o[i][0] = o[i][1] = 0.f;
+    const int b1 = src.b1;
+    int stage = 0;
+    for (int blk = src.first(warp); blk < b1; blk += src.kStep) {
+        copy_wait<kStages - 2>();
+        __syncwarp();                        // this batch is here for every lane, and all are done with the last
+        src.fetch(sm, warp, lane, blk + (kStages - 1) * src.kStep, stage == 0 ? kStages - 1 : stage - 1);
+        const uint8_t* kp = sm.ring[warp][stage][0];
+        const uint8_t* vp = sm.ring[warp][stage][1];
+        float ks[BB], ef[BB], vm[BB], inv[BB];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < C; ++c) kr[n][c] = ld_code16(kp + n * 8 * HD + 64 * c);
-        uint32_t vr[NT][2][VD / 4];          // keys 8 n + 2 t, + 1
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint8_t* p = vp + (n * 8 + e) * HD;
-                if constexpr (VD == 8) {
-                    const uint2 u = ld_code8(p);
-                    vr[n][e][0] = u.x; vr[n][e][1] = u.y;
-                } else {
-                    const uint4 u = ld_code16(p);
-                    vr[n][e][0] = u.x; vr[n][e][1] = u.y; vr[n][e][2] = u.z; vr[n][e][3] = u.w;
-                }
-            }
-        const float ks = __ldg(ksc + s / SPB) * kmul;
-        const float vs = __ldg(vsc + s / SPB);
-        // a block of zeros (scale 0): any reference serves, its codes add nothing to O
-        const float lv = vs == 0.f ? lv_ref : log2f(vs);
-        lv_ref = lv;
-        const float ivs = vs == 0.f ? exp2f(-lv) : __fdividef(1.0f, vs);
-        float w[NT][2], top = -INFINITY;
+        for (int b = 0; b < BB; ++b) {
+            ks[b] = sm.scale[warp][stage][0][b] * kmul;
+            const uint32_t vs = __float_as_uint(sm.scale[warp][stage][1][b]);
+            // 2^e m; a block of zeros (scale 0) adds nothing to O, and any e serves its share of the sum
+            int e = vs == 0u ? e_ref : (int)(vs >> 23) - 127;
+            const bool nan = e > 127;
+            e = nan ? 0 : e;
+            if (b == 0 || blk + b < b1) e_ref = e;
+            ef[b] = (float)e;
+            vm[b] = __uint_as_float((vs & 0x7fffffu) | (127u + 31u) << 23);
+            inv[b] = nan ? __uint_as_float(0x7fffffffu) : __uint_as_float((uint32_t)(127 - e) << 23);
+            if (b > 0 && blk + b >= b1) inv[b] = 0.f;
+        }
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+        // lane (g, t) ends with the score of head g % 4 and key 8 n + 2 t, + 1 for g >= 4
+        float s[NT], top = -INFINITY;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t acc[4] = {kMagicBits, kMagicBits, kMagicBits, kMagicBits};
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t word = (&kr[n][c].x)[i];
-                    mma16816(acc, qa[4 * c + i], codes_even(word), codes_odd(word));
-                }
-            w[n][0] = fmaf(acc[0] + acc[2], ks, lv);
-            w[n][1] = fmaf(acc[1] + acc[3], ks, lv);
-            top = fmaxf(top, fmaxf(w[n][0], w[n][1]));
+            for (int c = 0; c < C; ++c) {
+                const uint4 w = *reinterpret_cast<const uint4*>(kp + (8 * n + g) * HD + 16 * swizzled<HD>(8 * n + g, C * t + c));
+                mma_s8(acc, qa[2 * c], w.x, w.y);
+                mma_s8(acc, qa[2 * c + 1], w.z, w.w);
+            }
+            const float f0 = sum_of(acc[0], sm0) + sum_of(acc[2], sm1), f1 = sum_of(acc[1], sm0) + sum_of(acc[3], sm1);
+            s[n] = (up ? f1 : f0) + __shfl_xor_sync(0xffffffffu, up ? f0 : f1, 16);
+            const int b = n / (kQBlock / 8);
+            if (b > 0 && blk + b >= b1) s[n] = -INFINITY;
+            else top = fmaxf(top, fmaf(s[n], ks[b], ef[b]));
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        if (__any_sync(0xffffffffu, top > M)) {
-            const float Mn = fmaxf(M, top), f = ex2(M - Mn);
-            M = Mn;
-            l *= f;
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        const float Mn = fmaxf(M, top), f = ex2(M - Mn);
+        M = Mn;
+        l *= f;
+        uint32_t wp[NT];                     // the pair's digits
 #pragma unroll
-            for (int i = 0; i < VD; ++i)
+        for (int b = 0; b < BB; ++b) {
+            const float off = ef[b] - M;
+            float sum = 0.f;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[i][k] *= f;
-        }
-        const float off = kWeightBits - M;
-        uint32_t pa[NT / 2][4];
-        float sum = 0.f;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const float w0 = ex2(w[n][0] + off), w1 = ex2(w[n][1] + off);
-            sum += w0 + w1;
-            split2(w0, w1, pa[n / 2][(n & 1) * 2], pa[n / 2][(n & 1) * 2 + 1]);
-        }
-        l = fmaf(sum, ivs, l);
-#pragma unroll
-        for (int k = 0; k < NT / 2; ++k)
-#pragma unroll
-            for (int j = 0; j < VD / 4; ++j) {
-                // dims 4 j .. 4 j + 3 of the lane's: keys (2 t, 2 t + 1) and (2 t + 8, 2 t + 9) as pairs
-                const uint32_t x0 = vr[2 * k][0][j], y0 = vr[2 * k][1][j], x1 = vr[2 * k + 1][0][j], y1 = vr[2 * k + 1][1][j];
-                const uint32_t p0 = __byte_perm(x0, y0, 0x5410), r0 = __byte_perm(x0, y0, 0x7632);
-                const uint32_t p1 = __byte_perm(x1, y1, 0x5410), r1 = __byte_perm(x1, y1, 0x7632);
-                mma16816(o[4 * j], pa[k], codes_even(p0), codes_even(p1));
-                mma16816(o[4 * j + 1], pa[k], codes_odd(p0), codes_odd(p1));
-                mma16816(o[4 * j + 2], pa[k], codes_even(r0), codes_even(r1));
-                mma16816(o[4 * j + 3], pa[k], codes_odd(r0), codes_odd(r1));
+            for (int n = b * (kQBlock / 8); n < (b + 1) * (kQBlock / 8); ++n) {
+                const float w = b > 0 && blk + b >= b1 ? 0.f : ex2(fmaf(s[n], ks[b], off));
+                sum += w;
+                const uint32_t W = __float2uint_rn(w * vm[b]);
+                wp[n] = __byte_perm(W, __shfl_xor_sync(0xffffffffu, W, 16), sel_w);
             }
+            l = fmaf(sum, inv[b], l);
+        }
+        uint32_t pa[NT / 4][4];
+#pragma unroll
+        for (int k = 0; k < NT / 4; ++k)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                pa[k][2 * w] = __byte_perm(wp[4 * k + 2 * w], wp[4 * k + 2 * w + 1], 0x7632);
+                pa[k][2 * w + 1] = __byte_perm(wp[4 * k + 2 * w], wp[4 * k + 2 * w + 1], 0x5410);
+            }
+#pragma unroll
+        for (int j = 0; j < VD / 8; ++j) {
+            // dims 8 j .. 8 j + 7 of the lane's, in two words of each key
+            uint32_t acc[8][4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = kMagicBits;
+#pragma unroll
+            for (int k = 0; k < NT / 4; ++k) {
+                uint32_t bw[2][8];           // [half of the K step][dim]: that dim of four keys
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    uint2 x[4];              // keys 8 n + 2 t, + 1 of tiles n = 4 k + 2 w, + 1
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 8 * (4 * k + 2 * w + i / 2) + 2 * t + (HD == 64 ? (i & 1) ^ (t & 1) : i & 1);
+                        const int c = HD == 64 ? g >> 1 : g;
+                        x[i] = *reinterpret_cast<const uint2*>(vp + r * HD + 16 * swizzled<HD>(r, c) + (HD == 64 ? 8 * (g & 1) : 8 * j));
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t x0 = h ? x[0].y : x[0].x, x1 = h ? x[1].y : x[1].x;
+                        const uint32_t x2 = h ? x[2].y : x[2].x, x3 = h ? x[3].y : x[3].x;
+                        const uint32_t p = __byte_perm(x0, x1, sel_lo), q = __byte_perm(x2, x3, sel_lo);
+                        const uint32_t r = __byte_perm(x0, x1, sel_hi), u = __byte_perm(x2, x3, sel_hi);
+                        bw[w][4 * h] = __byte_perm(p, q, 0x5410);
+                        bw[w][4 * h + 1] = __byte_perm(p, q, 0x7632);
+                        bw[w][4 * h + 2] = __byte_perm(r, u, 0x5410);
+                        bw[w][4 * h + 3] = __byte_perm(r, u, 0x7632);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mma_u8(acc[i], pa[k], bw[0][i], bw[1][i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                o[8 * j + i][0] = fmaf(o[8 * j + i][0], f, sum_of(acc[i][0], vm0) + sum_of(acc[i][2], vm1));
+                o[8 * j + i][1] = fmaf(o[8 * j + i][1], f, sum_of(acc[i][1], vm0) + sum_of(acc[i][3], vm1));
+            }
+        }
     }
+    copy_wait<0>();
+    __syncwarp();
+    // the halves of the digits, and the lanes' shares of the sum (keys 2 t of tile n, or 2 t + 1)
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
-    if (g < a.group && g < kMaxGroupHeads) {
-        if (t == 0) {
-            sm.m[warp][g] = M;
-            sm.l[warp][g] = l;
-        }
-#pragma unroll
-        for (int i = 0; i < VD; ++i) {
-            sm.o[warp][g][(2 * t) * VD + i] = o[i][0] + o[i][2];
-            sm.o[warp][g][(2 * t + 1) * VD + i] = o[i][1] + o[i][3];
-        }
+    l += __shfl_xor_sync(0xffffffffu, l, 16);
+    if (g < a.group && t == 0) {
+        sm.m[warp][g] = M;
+        sm.l[warp][g] = l;
     }
+#pragma unroll
+    for (int i = 0; i < VD; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float x = o[i][e] + __shfl_xor_sync(0xffffffffu, o[i][e], 16);
+            if (g < a.group) sm.o(warp, g)[(2 * t + e) * VD + i] = x;
+        }
 }
 
 // The open block's n < 32 bf16 tokens, fp32 on the CUDA cores: warp h takes head h,
@@ -347,38 +469,56 @@ template <int HD>
 __device__ __forceinline__ void attn_tail(const AttnArgs& a, AttnSmem<HD>& sm, size_t plane, int n, int warp, int lane) {
     if (warp >= a.group) return;
     const uint16_t* kt = a.tail[0] + plane * (kQBlock * HD) + (size_t)min(lane, n - 1) * HD;
-    const uint16_t* vt = a.tail[1] + plane * (kQBlock * HD);
+    const uint16_t* vt = a.tail[1] + plane * (kQBlock * HD) + lane * (HD / 32);
+    // every load is issued before the first is used, half the values' behind the scores
+    constexpr int D = HD / 32, H = kQBlock / 2;
+    uint4 kr[HD / 8];
+    uint32_t vr[H][D / 2];
+#pragma unroll
+    for (int e = 0; e < HD / 8; ++e) kr[e] = *reinterpret_cast<const uint4*>(kt + 8 * e);
+#pragma unroll
+    for (int i = 0; i < H; ++i)
+#pragma unroll
+        for (int d = 0; d < D / 2; ++d) vr[i][d] = *reinterpret_cast<const uint32_t*>(vt + min(i, n - 1) * HD + 2 * d);
     float s = 0.f;
 #pragma unroll
-    for (int e = 0; e < HD; e += 8) {
-        const uint4 u = *reinterpret_cast<const uint4*>(kt + e);
+    for (int e = 0; e < HD / 8; ++e)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t w = (&u.x)[i];
-            s = fmaf(__uint_as_float(w << 16), sm.q[warp][e + 2 * i], s);
-            s = fmaf(__uint_as_float(w & 0xffff0000u), sm.q[warp][e + 2 * i + 1], s);
+            const uint32_t w = (&kr[e].x)[i];
+            s = fmaf(__uint_as_float(w << 16), sm.q[warp][8 * e + 2 * i], s);
+            s = fmaf(__uint_as_float(w & 0xffff0000u), sm.q[warp][8 * e + 2 * i + 1], s);
         }
-    }
-    s = lane < n ? s * (kLog2e * rsqrtf((float)HD)) : -INFINITY;
+    s = lane < n ? s * (kLog2e * (HD == 64 ? 0.125f : 0.08838834764831845f)) : -INFINITY;
     float m = s;
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
     m = fmaxf(m, -1e30f);
-    const float w = lane < n ? exp2f(s - m + kWeightBits) : 0.f;
+    const float w = lane < n ? exp2f(s - m) : 0.f;
     float l = w;
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-    constexpr int D = HD / 32;
     float o[D];
 #pragma unroll
     for (int d = 0; d < D; ++d) o[d] = 0.f;
-    for (int i = 0; i < n; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, w, i);
 #pragma unroll
-        for (int d = 0; d < D; d += 2) {
-            const uint32_t u = *reinterpret_cast<const uint32_t*>(vt + i * HD + lane * D + d);
-            o[d] = fmaf(wi, __uint_as_float(u << 16), o[d]);
-            o[d + 1] = fmaf(wi, __uint_as_float(u & 0xffff0000u), o[d + 1]);
+    for (int half = 0; half < 2; ++half) {
+        if (half * H >= n) break;
+        if (half == 1) {
+#pragma unroll
+            for (int i = 0; i < H; ++i)
+#pragma unroll
+                for (int d = 0; d < D / 2; ++d) vr[i][d] = *reinterpret_cast<const uint32_t*>(vt + min(H + i, n - 1) * HD + 2 * d);
+        }
+        // tokens behind the last (the last one's values) weigh nothing
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, half * H + i);
+#pragma unroll
+            for (int d = 0; d < D / 2; ++d) {
+                o[2 * d] = fmaf(wi, __uint_as_float(vr[i][d] << 16), o[2 * d]);
+                o[2 * d + 1] = fmaf(wi, __uint_as_float(vr[i][d] & 0xffff0000u), o[2 * d + 1]);
+            }
         }
     }
     if (lane == 0) {
@@ -386,7 +526,7 @@ __device__ __forceinline__ void attn_tail(const AttnArgs& a, AttnSmem<HD>& sm, s
         sm.l[kAttWarps][warp] = l;
     }
 #pragma unroll
-    for (int d = 0; d < D; ++d) sm.o[kAttWarps][warp][lane * D + d] = o[d];
+    for (int d = 0; d < D; ++d) sm.tail_o[warp][lane * D + d] = o[d];
 }
 
 // Joins the parts in sm whose mask bit is set. FINAL: the output row; else a partial.
@@ -405,7 +545,7 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, AttnSmem<HD>& sm, u
             if (parts >> p & 1) {
                 const float f = exp2f(sm.m[p][h] - M);
                 l = fmaf(f, sm.l[p][h], l);
-                x = fmaf(f, sm.o[p][h][d], x);
+                x = fmaf(f, sm.o(p, h)[d], x);
             }
         if (FINAL) {
             o[e] = x / l;
@@ -421,6 +561,12 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, AttnSmem<HD>& sm, u
 }
 
 template <int HD>
+__device__ __forceinline__ AttnSmem<HD>& attn_smem() {
+    extern __shared__ __align__(16) uint8_t attn_raw[];
+    return *reinterpret_cast<AttnSmem<HD>*>(attn_raw);
+}
+
+template <int HD>
 __device__ __forceinline__ void attn_load_q(const AttnArgs& a, AttnSmem<HD>& sm, int b, int h) {
     const float* q = a.q + ((size_t)b * a.n_heads + h) * a.group * HD;
     for (int e = threadIdx.x; e < a.group * HD; e += 32 * kAttWarps) (&sm.q[0][0])[e] = q[e];
@@ -432,90 +578,103 @@ __device__ __forceinline__ int attn_keys(const AttnArgs& a, int b) {
     return pos >= a.max_ctx ? a.max_ctx : max(pos, -1) + 1;
 }
 
-// How the blocks of all rows and KV heads, in that order, are cut over the CTAs of the
-// split: `units` blocks over `n` CTAs, CTA c taking [c units / n, (c + 1) units / n).
+__device__ __forceinline__ int attn_units(const AttnArgs& a, int b) { return (attn_keys(a, b) + kQBlock - 1) / kQBlock; }
+// A (row, KV head)'s share of the order: its blocks behind kPad units without work, which stand for what
+// starting and joining one more piece (its open block among it) costs the CTA that has them. 0 / 8 /
+// 16 / 24 / 32 units: 61.1 / 58.8 / 57.0 / 56.4 / 56.4 us at 4 x 60001 keys of 128 dims.
+constexpr int kPad = 24;
+__device__ __forceinline__ int attn_share(const AttnArgs& a, int b) {
+    const int n = attn_units(a, b);
+    return n ? n + kPad : 0;
+}
+
+// How the blocks (open ones included) of all rows and KV heads, in that order, are cut over
+// the CTAs of the split: `units` blocks over `n` CTAs, CTA c taking [c units / n,
+// (c + 1) units / n).
 struct SplitPlan {
     int units, n;
     __device__ __forceinline__ int start(int c) const { return (int)((long long)c * units / n); }
     __device__ __forceinline__ int owner(int u) const { return (int)(((long long)(u + 1) * n - 1) / units); }
 };
-constexpr int kMinUnits = kAttWarps;     // blocks per CTA at least
+template <int HD>
 __device__ __forceinline__ SplitPlan split_plan(const AttnArgs& a) {
     SplitPlan p{0, 0};
-    for (int b = 0; b < a.rows; ++b) p.units += attn_keys(a, b) / kQBlock * a.n_heads;
-    p.n = min(a.n_cta, (p.units + kMinUnits - 1) / kMinUnits);
+    for (int b = 0; b < a.rows; ++b) p.units += attn_share(a, b) * a.n_heads;
+    constexpr int least = kAttWarps * batch_blocks(HD);   // a batch for each warp
+    p.n = min(a.n_cta, (p.units + least - 1) / least);
     return p;
 }
 
-// One CTA per (row, KV head): all its blocks and its open block.
+// Blocks [u, stop) of one (row, KV head) with `keys` keys, the open one included, into the
+// parts of sm: which, as bits.
 template <int HD>
-__global__ void __launch_bounds__(32 * kAttWarps) k_attn_whole(const __grid_constant__ AttnArgs a) {
-    __shared__ AttnSmem<HD> sm;
-    const int h = blockIdx.x % a.n_heads, b = blockIdx.x / a.n_heads;
+__device__ __forceinline__ uint32_t attn_range(const AttnArgs& a, AttnSmem<HD>& sm, int b, int h, int u, int stop, int keys) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const size_t plane = ((size_t)a.layer * a.max_batch + b) * a.n_heads + h;
+    const int nb = keys / kQBlock;
+    const AttnSource<HD> src(a, plane, u, min(stop, nb));
+    src.start(sm, warp, lane);
+    attn_load_q(a, sm, b, h);
+    uint32_t parts = 0;
+    if (stop > nb) {
+        attn_tail<HD>(a, sm, plane, keys - nb * kQBlock, warp, lane);
+        parts = 1u << kAttWarps;
+    }
+    if (src.b0 < src.b1) {
+        attn_blocks<HD>(a, sm, src, warp, lane);
+        parts |= (1u << kAttWarps) - 1;
+    }
+    return parts;
+}
+
+// One CTA per (row, KV head): all its blocks.
+template <int HD>
+__global__ void __launch_bounds__(32 * kAttWarps, attn_per_sm(HD)) k_attn_whole(const __grid_constant__ AttnArgs a) {
+    AttnSmem<HD>& sm = attn_smem<HD>();
+    const int h = blockIdx.x % a.n_heads, b = blockIdx.x / a.n_heads;
+    cudaGridDependencySynchronize();     // everything enqueued before has run
     const int keys = attn_keys(a, b);
     float* out = a.out + ((size_t)b * a.n_heads + h) * a.group * HD;
     if (keys == 0) {
         for (int e = threadIdx.x; e < a.group * HD; e += 32 * kAttWarps) out[e] = 0.f;
         return;
     }
-    const size_t plane = ((size_t)a.layer * a.max_batch + b) * a.n_heads + h;
-    attn_load_q(a, sm, b, h);
-    const int nb = keys / kQBlock, nt = keys % kQBlock;
-    uint32_t parts = 0;
-    if (nb) {
-        attn_blocks<HD>(a, sm, plane, 0, nb, warp, lane);
-        parts = (1u << kAttWarps) - 1;
-    }
-    if (nt) {
-        attn_tail<HD>(a, sm, plane, nt, warp, lane);
-        parts |= 1u << kAttWarps;
-    }
+    const uint32_t parts = attn_range<HD>(a, sm, b, h, 0, attn_units(a, b), keys);
     attn_join<HD, true>(a, sm, parts, out, nullptr);
 }
 
 // The split: CTA c takes its range of blocks, which may cover several (row, KV head)
 // pairs; each piece becomes partial slot c + pair (distinct: both only grow along the
-// order of the blocks). The last rows * n_heads CTAs take the open blocks, slot
-// n_cta + pairs + pair.
+// order of the blocks).
 template <int HD>
-__global__ void __launch_bounds__(32 * kAttWarps) k_attn_split(const __grid_constant__ AttnArgs a) {
-    __shared__ AttnSmem<HD> sm;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int pairs = a.rows * a.n_heads;
-    if ((int)blockIdx.x < pairs) {
-        const int pair = blockIdx.x, b = pair / a.n_heads, h = pair % a.n_heads;
-        const int nt = attn_keys(a, b) % kQBlock;
-        if (nt) {
-            attn_load_q(a, sm, b, h);
-            attn_tail<HD>(a, sm, ((size_t)a.layer * a.max_batch + b) * a.n_heads + h, nt, warp, lane);
-            const size_t slot = (size_t)a.n_cta + pairs + pair;
-            attn_join<HD, false>(a, sm, 1u << kAttWarps, a.part_o + slot * a.group * HD, a.part_ml + slot * a.group * 2);
-        }
-    } else {
-        const int c = blockIdx.x - pairs;
-        const SplitPlan P = split_plan(a);
-        if (c < P.n) {
-            const int u0 = P.start(c), u1 = P.start(c + 1);
-            int first = 0;   // first unit of row b
-            for (int b = 0; b < a.rows && first < u1; ++b) {
-                const int nb = attn_keys(a, b) / kQBlock;
-                const int last = first + nb * a.n_heads;
-                for (int u = max(u0, first); u < min(u1, last);) {
-                    const int h = (u - first) / nb, base = first + h * nb;
-                    const int stop = min(u1, base + nb);
-                    attn_load_q(a, sm, b, h);
-                    attn_blocks<HD>(a, sm, ((size_t)a.layer * a.max_batch + b) * a.n_heads + h, u - base, stop - base, warp, lane);
+__global__ void __launch_bounds__(32 * kAttWarps, attn_per_sm(HD)) k_attn_split(const __grid_constant__ AttnArgs a) {
+    AttnSmem<HD>& sm = attn_smem<HD>();
+    // once every CTA runs, the joining kernel may be placed where CTAs end; it waits for them all
+    cudaTriggerProgrammaticLaunchCompletion();
+    cudaGridDependencySynchronize();     // everything enqueued before has run
+    const SplitPlan P = split_plan<HD>(a);
+    const int c = blockIdx.x;
+    if (c < P.n) {
+        const int u0 = P.start(c), u1 = P.start(c + 1);
+        int first = 0;   // first unit of row b
+        for (int b = 0; b < a.rows && first < u1; ++b) {
+            const int keys = attn_keys(a, b), share = attn_share(a, b);
+            const int last = first + share * a.n_heads;
+            for (int u = max(u0, first); u < min(u1, last);) {
+                const int h = (u - first) / share, base = first + h * share;
+                const int end = min(u1, base + share);
+                // without the padding; a piece of nothing but padding is no piece
+                const int from = max(u - base - kPad, 0), stop = end - base - kPad;
+                if (stop > from) {
+                    const uint32_t parts = attn_range<HD>(a, sm, b, h, from, stop, keys);
                     const size_t slot = (size_t)c + b * a.n_heads + h;
-                    attn_join<HD, false>(a, sm, (1u << kAttWarps) - 1, a.part_o + slot * a.group * HD,
-                                         a.part_ml + slot * a.group * 2);
-                    u = stop;
+                    attn_join<HD, false>(a, sm, parts, a.part_o + slot * a.group * HD, a.part_ml + slot * a.group * 2);
                 }
-                first = last;
+                u = end;
             }
+            first = last;
         }
     }
-    cudaTriggerProgrammaticLaunchCompletion();
 }
 
 // Joins the partials of one (row, query head): warps take slots in turn, lanes the dims.
@@ -526,20 +685,19 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_merge_q(const __grid_c
     __shared__ float so[kJoinWarps][HD], sm[kJoinWarps], sl[kJoinWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int heads = a.n_heads * a.group, b = blockIdx.x / heads, hq = blockIdx.x % heads;
-    const int h = hq / a.group, hg = hq % a.group, pairs = a.rows * a.n_heads, pair = b * a.n_heads + h;
-    const int keys = attn_keys(a, b), nb = keys / kQBlock, nt = keys % kQBlock;
-    const SplitPlan P = split_plan(a);
+    const int h = hq / a.group, hg = hq % a.group, pair = b * a.n_heads + h;
+    const int share = attn_share(a, b);
+    const SplitPlan P = split_plan<HD>(a);
     int first = 0;
-    for (int i = 0; i < b; ++i) first += attn_keys(a, i) / kQBlock * a.n_heads;
-    first += h * nb;
-    const int c0 = nb ? P.owner(first) : 0, n = nb ? P.owner(first + nb - 1) - c0 + 1 : 0;
-    const int total = n + (nt ? 1 : 0);
+    for (int i = 0; i < b; ++i) first += attn_share(a, i) * a.n_heads;
+    first += h * share;
+    const int c0 = share ? P.owner(first + kPad) : 0, total = share ? P.owner(first + share - 1) - c0 + 1 : 0;
     cudaGridDependencySynchronize();
     float M = -INFINITY, l = 0.f, o[D];
 #pragma unroll
     for (int d = 0; d < D; ++d) o[d] = 0.f;
     for (int i = warp; i < total; i += kJoinWarps) {
-        const size_t slot = i < n ? (size_t)c0 + i + pair : (size_t)a.n_cta + pairs + pair;
+        const size_t slot = (size_t)c0 + i + pair;
         const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (slot * a.group + hg) * 2);
         const float* p = a.part_o + (slot * a.group + hg) * HD + lane * D;
         const float Mn = fmaxf(M, ml.x), f = exp2f(M - Mn), w = exp2f(ml.x - Mn);
@@ -575,30 +733,40 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_merge_q(const __grid_c
 
 // ------------------------------------------------------------------ launches
 
-constexpr int kSplitCtas = kQSms * 3;
 constexpr int kWholeCtx = 512;    // contexts up to here run one CTA per (row, head)
 
 bool attn_is_split(int max_ctx) { return max_ctx > kWholeCtx; }
-size_t attn_slots(int rows, int n_heads) { return (size_t)kSplitCtas + 2 * (size_t)rows * n_heads; }
+int attn_ctas(int hd) { return kQSms * attn_per_sm(hd); }
+size_t attn_slots(int hd, int rows, int n_heads) { return (size_t)attn_ctas(hd) + (size_t)rows * n_heads; }
 
-template <int HD>
-cudaError_t attn_launch(AttnArgs& a, cudaStream_t st) {
-    if (a.n_cta == 0) {
-        k_attn_whole<HD><<<a.rows * a.n_heads, 32 * kAttWarps, 0, st>>>(a);
-        return cudaGetLastError();
-    }
-    k_attn_split<HD><<<a.n_cta + a.rows * a.n_heads, 32 * kAttWarps, 0, st>>>(a);
+// A kernel that may be placed while the one before it in the stream still ends; each waits for
+// all of it (cudaGridDependencySynchronize) before it reads or writes anything.
+template <class... P, class... A>
+cudaError_t launch_behind(void (*kernel)(P...), int grid, int block, int smem, cudaStream_t st, A&&... args) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(a.rows * a.n_heads * a.group));
-    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = st;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_attn_merge_q<HD>, static_cast<const AttnArgs>(a));
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int HD>
+cudaError_t attn_launch(const AttnArgs& a, cudaStream_t st) {
+    const int smem = (int)sizeof(AttnSmem<HD>);
+    const bool whole = a.n_cta == 0;
+    const void* f = whole ? (const void*)k_attn_whole<HD> : (const void*)k_attn_split<HD>;
+    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (whole) return launch_behind(k_attn_whole<HD>, a.rows * a.n_heads, 32 * kAttWarps, smem, st, a);
+    e = launch_behind(k_attn_split<HD>, a.n_cta, 32 * kAttWarps, smem, st, a);
+    if (e != cudaSuccess) return e;
+    return launch_behind(k_attn_merge_q<HD>, a.rows * a.n_heads * a.group, 32 * kJoinWarps, 0, st, a);
 }
 
 }  // namespace
@@ -653,7 +821,7 @@ extern "C" size_t mk_qcache_attention_workspace(const mk_qcache* c, int rows, in
         n_heads % c->n_kv_heads != 0 || n_heads / c->n_kv_heads > mk::kMaxGroupHeads || max_ctx < 1 ||
         max_ctx > c->max_seq || !mk::attn_is_split(max_ctx))
         return 0;
-    const size_t slots = mk::attn_slots(rows, c->n_kv_heads) * (size_t)(n_heads / c->n_kv_heads);
+    const size_t slots = mk::attn_slots(c->head_dim, rows, c->n_kv_heads) * (size_t)(n_heads / c->n_kv_heads);
     return slots * (size_t)(c->head_dim + 2) * sizeof(float);
 }
 
@@ -688,9 +856,9 @@ extern "C" mk_status mk_qcache_attention(const mk_qcache* c, int layer, int rows
     a.positions = positions;
     a.out = out;
     if (need) {
-        a.n_cta = mk::kSplitCtas;
+        a.n_cta = mk::attn_ctas(c->head_dim);
         a.part_ml = static_cast<float*>(workspace);
-        a.part_o = a.part_ml + mk::attn_slots(rows, c->n_kv_heads) * (size_t)a.group * 2;
+        a.part_o = a.part_ml + mk::attn_slots(c->head_dim, rows, c->n_kv_heads) * (size_t)a.group * 2;
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = c->head_dim == 64 ? mk::attn_launch<64>(a, st) : mk::attn_launch<128>(a, st);

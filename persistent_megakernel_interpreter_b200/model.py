@@ -29,10 +29,15 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _here(*tensors) -> bool:
-    """Whether all of them are on the calling thread's current device, where the calls run."""
-    device = torch.cuda.current_device()
-    return all(t.is_cuda and t.get_device() == device for t in tensors)
+def _at(t: torch.Tensor, dtype: torch.dtype, n: int, device: int) -> int:
+    """The address of a contiguous tensor of at least ``n`` elements on ``device``."""
+    assert t.dtype is dtype and t.get_device() == device and t.numel() >= n and t.is_contiguous(), \
+        f"a contiguous {dtype} tensor of {n} elements or more on cuda:{device} is wanted"
+    return t.data_ptr()
+
+
+def _raw_stream(stream, device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
 
 
 class Megakernel:
@@ -133,22 +138,18 @@ class Megakernel:
         """One step as ordinary kernels on an 8-bit cache (``qcache.QCache``); it needs no schedule, and
         contexts may be as long as the cache. ``status`` (int32 [1], optional) receives the step's
         device status. Without a ``workspace`` one is allocated for the call."""
-        assert _here(tokens, positions, logits)
-        for t, dt in ((tokens, torch.int32), (positions, torch.int32), (logits, torch.float32)):
-            assert t.dtype == dt and t.is_contiguous()
+        device = torch.cuda.current_device()
         batch = tokens.numel()
-        assert positions.numel() >= batch and logits.numel() >= batch * self.cfg.vocab
-        if status is not None:
-            assert _here(status) and status.dtype == torch.int32
         max_ctx = min(cache.max_seq, self.max_seq) if max_ctx is None else max_ctx
         if workspace is None:
-            with torch.cuda.stream(stream or torch.cuda.current_stream()):
+            with torch.cuda.stream(stream or torch.cuda.current_stream()):  # given back in that stream's order
                 workspace = self.decode_step_qcache_workspace(cache, batch, max_ctx)
-        assert _here(workspace) and workspace.is_contiguous()
         _lib.check(_lib.lib().mk_decode_step_qcache(
-            self._h, cache._ref, batch, max_ctx, _ptr(tokens), _ptr(positions), _ptr(logits), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _ptr(status) if status is not None else None,
-            _stream(stream)), "mk_decode_step_qcache")
+            self._h, cache._ref, batch, max_ctx, _at(tokens, torch.int32, batch, device),
+            _at(positions, torch.int32, batch, device), _at(logits, torch.float32, batch * self.cfg.vocab, device),
+            _at(workspace, torch.uint8, 1, device), workspace.numel(),
+            None if status is None else _at(status, torch.int32, 1, device), _raw_stream(stream, device)),
+            "mk_decode_step_qcache")
 
     def decode_steps_beam(self, tokens, positions, cache, logits, scores, n_steps: int, finished=None, eos: int = -1,
                           starts=None, generated=None, parents=None, max_ctx: int | None = None, workspace=None,
@@ -251,25 +252,22 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, next_tokens: torch.T
     ``eos`` at its own score; ``next_finished`` receives who is finished then. ``positions``
     (optional, one per row) are advanced by one. ``next_scores`` may be ``scores`` and
     ``next_finished`` may be ``finished``."""
-    assert _here(logits, scores, next_tokens, parents, next_scores)
-    assert logits.dtype == torch.float32 and logits.dim() == 2 and (logits.stride(1) == 1 or logits.shape[1] == 1)
-    assert scores.dtype == torch.float32 and scores.dim() == 2 and scores.is_contiguous()
+    device = torch.cuda.current_device()
+    rows, vocab = logits.shape
     batch, beams = scores.shape
-    assert logits.shape[0] == batch * beams and next_tokens.dim() == 2
-    n_out = next_tokens.shape[1]
-    for t, dt in ((next_tokens, torch.int32), (parents, torch.int32), (next_scores, torch.float32)):
-        assert t.dtype == dt and t.shape == (batch, n_out) and t.is_contiguous()
-    for t, shape in ((finished, scores.shape), (next_finished, next_tokens.shape)):
-        assert t is None or (_here(t) and t.dtype == torch.int32 and t.shape == shape and t.is_contiguous())
-    if positions is not None:
-        assert _here(positions) and positions.dtype == torch.int32 and positions.numel() >= batch * beams
-        assert positions.is_contiguous()
-    stride = logits.stride(0) if logits.shape[0] > 1 else max(logits.stride(0), logits.shape[1])
+    out_batch, n_out = next_tokens.shape
+    n_in, n = batch * beams, batch * n_out
+    assert rows == n_in and out_batch == batch and logits.get_device() == device and logits.dtype is torch.float32
+    stride, inner = logits.stride()
+    assert inner == 1 or vocab == 1
     _lib.check(_lib.lib().mk_beam_select(
-        _ptr(logits), stride, batch, beams, logits.shape[1], n_out, _ptr(scores),
-        _ptr(finished) if finished is not None else None, eos, _ptr(next_tokens), _ptr(parents), _ptr(next_scores),
-        _ptr(next_finished) if next_finished is not None else None,
-        _ptr(positions) if positions is not None else None, _stream(stream)), "mk_beam_select")
+        logits.data_ptr(), stride if rows > 1 else vocab, batch, beams, vocab, n_out,
+        _at(scores, torch.float32, n_in, device), None if finished is None else _at(finished, torch.int32, n_in, device),
+        eos, _at(next_tokens, torch.int32, n, device), _at(parents, torch.int32, n, device),
+        _at(next_scores, torch.float32, n, device),
+        None if next_finished is None else _at(next_finished, torch.int32, n, device),
+        None if positions is None else _at(positions, torch.int32, n_in, device), _raw_stream(stream, device)),
+        "mk_beam_select")
 
 
 def cache_reorder(k_cache: torch.Tensor, v_cache: torch.Tensor, parents: torch.Tensor, lengths: torch.Tensor,
@@ -278,16 +276,16 @@ def cache_reorder(k_cache: torch.Tensor, v_cache: torch.Tensor, parents: torch.T
     starts[r] .. lengths[parents[r]] - 1, all rows at once and in place, asynchronous on ``stream``: beams
     that follow ``beam_select``, a sequence forked into free rows, live rows moved over finished ones.
     A parent that is the row itself or no row (-1) leaves the row as it is."""
-    from .qcache import _check_rows
-    assert _here(k_cache, v_cache) and k_cache.dtype == torch.bfloat16 and v_cache.dtype == torch.bfloat16
-    assert k_cache.dim() == 5 and v_cache.shape == k_cache.shape
-    assert k_cache.is_contiguous() and v_cache.is_contiguous()
-    rows = _check_rows(parents, lengths, starts)
+    device = torch.cuda.current_device()
+    rows = parents.numel()
     n_layers, max_batch, heads, max_seq, dim = k_cache.shape
+    assert v_cache.shape == k_cache.shape
     cfg = _lib.MkConfig(n_layers, 0, 0, heads, dim, 0, 0, 0.0, 0.0, max_batch, max_seq)
-    _lib.check(_lib.lib().mk_cache_reorder(ctypes.byref(cfg), _ptr(k_cache), _ptr(v_cache), rows, _ptr(parents),
-                                           _ptr(lengths), _ptr(starts) if starts is not None else None,
-                                           _stream(stream)), "mk_cache_reorder")
+    _lib.check(_lib.lib().mk_cache_reorder(
+        ctypes.byref(cfg), _at(k_cache, torch.bfloat16, 1, device), _at(v_cache, torch.bfloat16, 1, device), rows,
+        _at(parents, torch.int32, rows, device), _at(lengths, torch.int32, rows, device),
+        None if starts is None else _at(starts, torch.int32, rows, device), _raw_stream(stream, device)),
+        "mk_cache_reorder")
 
 
 def plan_schedule(cfg: ModelConfig, batch: int, max_ctx: int, n_sm: int, max_batch: int = 8,

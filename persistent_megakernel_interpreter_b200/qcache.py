@@ -15,9 +15,10 @@ import torch
 
 from . import _lib
 from .config import ModelConfig
-from .model import _here, _ptr, _stream
+from .model import _at, _raw_stream
 
 BLOCK = _lib.QCACHE_BLOCK
+_Strides = ctypes.c_int64 * 4
 
 
 class QCache:
@@ -53,34 +54,40 @@ class QCache:
             assert t.device == k_codes.device
         self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
         self.k_tail, self.v_tail = k_tail, v_tail
-        self.n_layers, self.max_batch, self.n_kv_heads, self.max_seq, self.head_dim = k_codes.shape
-        self.device = k_codes.device
-        self._c = _lib.MkQcache(n_layers, max_batch, n_heads, max_seq, dim, 0, _ptr(k_codes), _ptr(v_codes),
-                                _ptr(k_scale), _ptr(v_scale), _ptr(k_tail), _ptr(v_tail))
+        self.n_layers, self.max_batch, self.n_kv_heads, self.max_seq, self.head_dim = tuple(k_codes.shape)
+        self.device, self._device = k_codes.device, k_codes.get_device()
+        self._c = _lib.MkQcache(n_layers, max_batch, n_heads, max_seq, dim, 0, k_codes.data_ptr(),
+                                v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k_tail.data_ptr(),
+                                v_tail.data_ptr())
         self._ref = ctypes.byref(self._c)
 
     def append(self, k, v, positions, counts=None, first_layer: int = 0, stream=None) -> None:
         """Stores ``k`` and ``v`` (bf16 [layers][rows][heads][tokens][dim], any strides with the dims
         contiguous) from slot ``positions[row]`` on: ``counts[row]`` tokens of each row (all of them
         where ``counts`` is None), in layers ``first_layer`` on."""
-        assert _here(k, v, positions) and k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16
-        layers, rows, heads, tokens, dim = k.shape
-        assert v.shape == k.shape and heads == self.n_kv_heads and dim == self.head_dim
-        strides = [s if n > 1 else 0 for s, n in zip(k.stride(), k.shape)]
-        assert strides == [s if n > 1 else 0 for s, n in zip(v.stride(), v.shape)] and strides[4] == 1
-        assert positions.dtype == torch.int32 and positions.is_contiguous() and positions.numel() >= rows
-        if counts is not None:
-            assert _here(counts) and counts.dtype == torch.int32 and counts.is_contiguous() and counts.numel() >= rows
+        device = torch.cuda.current_device()
+        layers, rows, heads, tokens, dim = shape = k.shape
+        strides = k.stride()
+        assert v.shape == shape and heads == self.n_kv_heads and dim == self.head_dim and strides[4] == 1
+        assert k.dtype is torch.bfloat16 and v.dtype is torch.bfloat16
+        assert k.get_device() == device and v.get_device() == device and self._device == device
+        strides = [s if n > 1 else 0 for s, n in zip(strides, shape)]
+        assert v.stride() == k.stride() or strides == [s if n > 1 else 0 for s, n in zip(v.stride(), shape)]
         _lib.check(_lib.lib().mk_qcache_append(
-            self._ref, first_layer, layers, rows, tokens, _ptr(k), _ptr(v), (ctypes.c_int64 * 4)(*strides[:4]),
-            _ptr(positions), _ptr(counts) if counts is not None else None, _stream(stream)), "mk_qcache_append")
+            self._ref, first_layer, layers, rows, tokens, k.data_ptr(), v.data_ptr(), _Strides(*strides[:4]),
+            _at(positions, torch.int32, rows, device),
+            None if counts is None else _at(counts, torch.int32, rows, device), _raw_stream(stream, device)),
+            "mk_qcache_append")
 
     def reorder(self, parents, lengths, starts=None, stream=None) -> None:
         """Row r takes over row parents[r]'s slots starts[r] .. lengths[parents[r]] - 1, all rows at once."""
-        rows = _check_rows(parents, lengths, starts)
-        _lib.check(_lib.lib().mk_qcache_reorder(self._ref, rows, _ptr(parents), _ptr(lengths),
-                                                _ptr(starts) if starts is not None else None, _stream(stream)),
-                   "mk_qcache_reorder")
+        device = torch.cuda.current_device()
+        rows = parents.numel()
+        assert self._device == device
+        _lib.check(_lib.lib().mk_qcache_reorder(
+            self._ref, rows, _at(parents, torch.int32, rows, device), _at(lengths, torch.int32, rows, device),
+            None if starts is None else _at(starts, torch.int32, rows, device), _raw_stream(stream, device)),
+            "mk_qcache_reorder")
 
     def attention_workspace(self, rows: int, n_heads: int, max_ctx: int):
         """A workspace for ``attention`` calls of this size, or None where they need none. Calls that
@@ -92,11 +99,10 @@ class QCache:
         """out[row][head] = attention of q[row][head] (fp32 [rows][n_heads][dim]) over slots
         0 .. positions[row] of ``layer``; a negative position gives zeros. ``max_ctx``: no row has more
         slots (max_seq where None). Without a ``workspace`` one is allocated for the call."""
-        assert _here(q, positions, out) and q.dtype == torch.float32 and out.dtype == torch.float32
-        assert q.is_contiguous() and out.is_contiguous() and q.dim() == 3 and q.shape == out.shape
+        device = torch.cuda.current_device()
         rows, n_heads, dim = q.shape
-        assert dim == self.head_dim and positions.dtype == torch.int32 and positions.is_contiguous()
-        assert positions.numel() >= rows
+        n = rows * n_heads * dim
+        assert dim == self.head_dim and self._device == device
         max_ctx = self.max_seq if max_ctx is None else max_ctx
         if workspace is None:
             if stream is None:
@@ -104,17 +110,10 @@ class QCache:
             else:
                 with torch.cuda.stream(stream):  # its memory is given back in the order of that stream
                     workspace = self.attention_workspace(rows, n_heads, max_ctx)
-        size = 0
+        at, size = None, 0
         if workspace is not None:
-            assert _here(workspace) and workspace.is_contiguous()
-            size = workspace.numel() * workspace.element_size()
+            at, size = _at(workspace, torch.uint8, 1, device), workspace.numel()
         _lib.check(_lib.lib().mk_qcache_attention(
-            self._ref, layer, rows, n_heads, max_ctx, _ptr(q), _ptr(positions), _ptr(out),
-            _ptr(workspace) if size else None, size, _stream(stream)), "mk_qcache_attention")
-
-
-def _check_rows(parents, lengths, starts) -> int:
-    rows = parents.numel()
-    for t in (parents, lengths) if starts is None else (parents, lengths, starts):
-        assert _here(t) and t.dtype == torch.int32 and t.is_contiguous() and t.numel() >= rows
-    return rows
+            self._ref, layer, rows, n_heads, max_ctx, _at(q, torch.float32, n, device),
+            _at(positions, torch.int32, rows, device), _at(out, torch.float32, n, device), at, size,
+            _raw_stream(stream, device)), "mk_qcache_attention")
