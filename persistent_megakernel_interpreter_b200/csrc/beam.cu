@@ -8,19 +8,21 @@
 // raw logits while the sum is formed, in one pass over HBM (bound: 4 bytes a logit);
 // only those few meet the other beams, as totals in 64 bits.
 //
-// One cluster per sequence. A row is cut into `splits` pieces at multiples of four
-// tokens, by token number and never by address, so equal rows give equal sums
-// wherever they lie. The cluster's CTAs take the pieces in turn:
-//   1. each thread keeps the maximum and the running sum of its logits; the n-th
-//      largest of 32 group maxima is a bound that at least n logits reach;
-//   2. the logits that reach it (few: the expected number is about n) are gathered by
-//      the threads whose maximum does, and ranked by counting.
+// One cluster per sequence. The rows of its unfinished beams are cut into equal pieces, by token
+// number and never by address, so equal rows give equal sums wherever they lie; a CTA takes a piece:
+//   1. thread t reads tokens t, t + T, .. (every alignment alike: a warp reads 128 bytes in a row)
+//      and keeps their maximum and running sum; from the maxima of 128 groups comes a bound that at least n
+//      logits reach;
+//   2. of the threads whose maximum reaches it (about n), each one's tokens are read again by its whole
+//      warp at once, and what reaches the bound (about n) is gathered and ranked by counting.
 // Each piece's maximum, sum and candidates go to CTA 0's shared memory (distributed
 // shared memory), which ranks them all by total and writes the answer.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <utility>
 
 #include "qcache.h"
 
@@ -29,20 +31,18 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kBeamThreads = 512;
-constexpr int kBeamWarps = kBeamThreads / 32;
 constexpr int kMaxBeams = 16;
 constexpr int kMaxOut = 32;
-constexpr int kMaxCluster = 8;
-constexpr int kMaxPieces = 16;            // pieces of a sequence's rows: beams * splits
+constexpr int kMaxPieces = 16;            // pieces of a sequence's rows: rows * splits
 constexpr int kList = 1024;               // gathered logits of a piece
+constexpr int kLoads = 32;                // logits a thread has on the way at once
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kBig = 3.402823466e38f;
 
 struct BeamArgs {
     const float* logits;
     long long ld;
-    int batch, beams, vocab, n_out, splits, piece, eos;
+    int batch, beams, vocab, n_out, eos;
     const float* scores;
     const int32_t* finished;
     int32_t* next_tokens;
@@ -57,21 +57,23 @@ struct Cand {
     int token;
 };
 
+// A candidate as two whole numbers that order it: its total, then beam, logit and token.
+struct alignas(16) Key {
+    unsigned long long total, tie;
+};
+
 struct BeamSmem {
     // CTA 0's: what every piece found
     Cand cand[kMaxPieces][kMaxOut];
     float m[kMaxPieces], s[kMaxPieces];
-    int count[kMaxPieces];
+    Key key[kMaxPieces * kMaxOut];
     // each CTA's own
     Cand list[kList];
-    float gmax[32], wm[kBeamWarps], ws[kBeamWarps];
-    int wcount[kBeamWarps];
+    alignas(16) float gmax[128];
+    float wm[16], ws[16];
+    int wcount[16];
     int n_list, n_tail;
     float again;
-    // the last step's
-    double m_row[kMaxBeams], log_row[kMaxBeams];
-    unsigned long long total[kMaxPieces * kMaxOut], tie[kMaxPieces * kMaxOut];
-    int2 from[kMaxOut];                   // parent row, finished
 };
 
 // Whole numbers in the order of the numbers; -0 becomes 0 first, for the two are equal.
@@ -84,23 +86,9 @@ __device__ __forceinline__ unsigned long long ordered(double x) {
     return u >> 63 ? ~u : u | 0x8000000000000000ull;
 }
 
-// x with NaN as -infinity: never chosen, adds nothing to the sum.
+// x with NaN as -infinity: never chosen, adds nothing to the sum. (Maxima and comparisons pass NaN over
+// by themselves; only sums need this, and only where there is one.)
 __device__ __forceinline__ float clean(float x) { return fmaxf(x, -INFINITY); }
-
-// Four consecutive logits of a row from token i (a multiple of 4); past the end -infinity.
-template <bool ALIGNED>
-__device__ __forceinline__ float4 load4(const float* row, int i, int end) {
-    if (ALIGNED && i + 4 <= end) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(row + i));
-        return make_float4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
-    }
-    float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-    if (i < end) v.x = clean(__ldg(row + i));
-    if (i + 1 < end) v.y = clean(__ldg(row + i + 1));
-    if (i + 2 < end) v.z = clean(__ldg(row + i + 2));
-    if (i + 3 < end) v.w = clean(__ldg(row + i + 3));
-    return v;
-}
 
 __device__ __forceinline__ float e2(float x) {
     float y;
@@ -111,114 +99,163 @@ __device__ __forceinline__ float e2(float x) {
 // of the type's lowest value keeps it.
 __device__ __forceinline__ float finite(float m) { return fminf(fmaxf(m, -kBig), kBig); }
 
-__device__ __forceinline__ void join_sum(float& m, float& s, float m2, float s2) {
-    const float M = fmaxf(m, m2), ref = finite(M);
-    s = s * e2((m - ref) * kLog2E) + s2 * e2((m2 - ref) * kLog2E);
+// The joint maximum and sum of N lanes: the maximum first, then each sum is rescaled once.
+template <int N>
+__device__ __forceinline__ void join_lanes(float& m, float& s) {
+    float M = m;
+#pragma unroll
+    for (int k = N / 2; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+    s *= e2((m - finite(M)) * kLog2E);
+#pragma unroll
+    for (int k = N / 2; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
     m = M;
 }
 
-// The n-th largest of 32 values (one per lane), equal ones counted by lane.
-__device__ __forceinline__ float nth_of_warp(float v, int n, int lane) {
-    int rank = 0;
+// A value that at least n of 128 (four per lane) reach, as large as it is cheap to find.
+__device__ __forceinline__ float bound_of(float4 v, int n, int lane) {
+    if (n <= 8) {
+        // the n-th largest of the 32 lanes' maxima, equal ones counted by lane: about n logits of a row reach it
+        const float x = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+        int rank = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const float o = __shfl_sync(0xffffffffu, v, i);
-        rank += o > v || (o == v && i < lane);
+        for (int i = 0; i < 32; ++i) {
+            const float o = __shfl_sync(0xffffffffu, x, i);
+            rank += o > x || (o == x && i < lane);
+        }
+        return __shfl_sync(0xffffffffu, x, __ffs(__ballot_sync(0xffffffffu, rank == n - 1)) - 1);
     }
-    return __shfl_sync(0xffffffffu, v, __ffs(__ballot_sync(0xffffffffu, rank == n - 1)) - 1);
+    // more are wanted: the n-th of 32 maxima would let many times n through. The n-th largest of all 128, to
+    // 20 bits (rounded down), bit by bit
+    const uint32_t k[4] = {ordered(v.x), ordered(v.y), ordered(v.z), ordered(v.w)};
+    uint32_t t = 0;
+    for (int bit = 31; bit >= 12; --bit) {
+        const uint32_t c = t | 1u << bit;
+        if ((int)__reduce_add_sync(0xffffffffu, (k[0] >= c) + (k[1] >= c) + (k[2] >= c) + (k[3] >= c)) >= n) t = c;
+    }
+    if (t <= ordered(-INFINITY)) return -INFINITY;
+    return __uint_as_float(t >> 31 ? t & 0x7fffffffu : ~t);
 }
 
-// Piece [begin, end) of one row: its maximum and sum, and its n best logits (fewer if it is
-// shorter), best first, equal logits by token. Into (out, *om, *os, *on) by all threads.
-template <bool ALIGNED>
-__device__ __forceinline__ void scan_piece(BeamSmem& sm, const float* row, int begin, int end, int n, Cand* out, float* om,
-                                           float* os, int* on) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    n = min(n, end - begin);
-    float m = -INFINITY, s = 0.f;
-    constexpr int U = 4;
-    for (int i = begin + 4 * tid; i < end; i += 4 * U * kBeamThreads) {
-        float4 v[U];
-        float bm = -INFINITY;
+// A thread's share of tokens [begin, end): begin + t, begin + t + T, ..; its maximum and sum.
+template <int T, bool CLEAN>
+__device__ __forceinline__ void scan_tokens(const float* row, int begin, int end, float& m, float& s) {
+    m = -INFINITY;
+    s = 0.f;
+    for (int i = begin + threadIdx.x; i < end; i += T * kLoads) {
+        float v[kLoads], bm = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            v[u] = load4<ALIGNED>(row, i + 4 * u * kBeamThreads, end);
-            bm = fmaxf(bm, fmaxf(fmaxf(v[u].x, v[u].y), fmaxf(v[u].z, v[u].w)));
+        for (int u = 0; u < kLoads; ++u) v[u] = i + u * T < end ? __ldg(row + i + u * T) : -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            if (CLEAN) v[u] = clean(v[u]);
+            bm = fmaxf(bm, v[u]);
         }
         if (bm > m) {
             s *= e2((m - finite(bm)) * kLog2E);
             m = bm;
         }
         const float ref = finite(m);
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            s += (e2((v[u].x - ref) * kLog2E) + e2((v[u].y - ref) * kLog2E)) +
-                 (e2((v[u].z - ref) * kLog2E) + e2((v[u].w - ref) * kLog2E));
+        for (int u = 0; u < kLoads; ++u) part[u & 3] += e2((v[u] - ref) * kLog2E);
+        s += (part[0] + part[1]) + (part[2] + part[3]);
     }
-    // group maxima (16 threads), then the CTA's maximum and sum
+}
+
+// Piece [begin, end) of one row: its maximum and sum, and its n best logits, best first, equal logits by
+// token (padded with tokens -1 if it is shorter), into (out, *om, *os) by all threads.
+template <int T>
+__device__ __forceinline__ void scan_piece(BeamSmem& sm, const float* row, int begin, int end, int want, Cand* out, float* om,
+                                           float* os) {
+    constexpr int W = T / 32, GROUP = T / 128;   // warps; threads that share a group maximum
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n = min(want, end - begin);
+    float m, s;
+    scan_tokens<T, false>(row, begin, end, m, s);
     float gm = m;
 #pragma unroll
-    for (int k = 8; k > 0; k >>= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, k));
+    for (int k = GROUP / 2; k > 0; k >>= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, k));
     float cm = m, cs = s;
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, cm, k), s2 = __shfl_xor_sync(0xffffffffu, cs, k);
-        join_sum(cm, cs, m2, s2);
-    }
-    if ((lane & 15) == 0) sm.gmax[tid >> 4] = gm;
+    join_lanes<32>(cm, cs);
+    if ((lane & (GROUP - 1)) == 0) sm.gmax[tid / GROUP] = gm;
     if (lane == 0) {
         sm.wm[warp] = cm;
         sm.ws[warp] = cs;
     }
     if (tid == 0) sm.n_list = 0;
     __syncthreads();
-    const float top = sm.gmax[lane];
-    float bound = n > 0 ? nth_of_warp(top, n, lane) : INFINITY;
-    // infinite logits share the row: the sum is their number
-    const bool endless = __any_sync(0xffffffffu, top == INFINITY);
-    if (endless) {
-        if (tid == 0) sm.n_tail = 0;
-        __syncthreads();
-        if (m == INFINITY) {
-            int k = 0;
-            for (int i = begin + 4 * tid; i < end; i += 4 * kBeamThreads) {
-                const float4 v = load4<ALIGNED>(row, i, end);
-                k += (v.x == INFINITY) + (v.y == INFINITY) + (v.z == INFINITY) + (v.w == INFINITY);
-            }
-            atomicAdd(&sm.n_tail, k);
+    float bound = n > 0 ? bound_of(reinterpret_cast<const float4*>(sm.gmax)[lane], n, lane) : INFINITY;
+    auto joined = [&] {
+        cm = lane < W ? sm.wm[lane] : -INFINITY;
+        cs = lane < W ? sm.ws[lane] : 0.f;
+        join_lanes<W>(cm, cs);
+        cm = __shfl_sync(0xffffffffu, cm, 0);
+        cs = __shfl_sync(0xffffffffu, cs, 0);
+    };
+    joined();
+    if (!(cs <= kBig)) {
+        // NaN or infinite logits (every warp sees the same sum): once more without the first, and infinite
+        // ones share the row, so that the sum is their number
+        scan_tokens<T, true>(row, begin, end, m, s);
+        if (cm == INFINITY) {
+            s = 0.f;
+            for (int i = begin + tid; i < end; i += T) s += __ldg(row + i) == INFINITY;
         }
         __syncthreads();
-    }
-    if (warp == 0) {
-        cm = lane < kBeamWarps ? sm.wm[lane] : -INFINITY;
-        cs = lane < kBeamWarps ? sm.ws[lane] : 0.f;
+        const bool endless = cm == INFINITY;
+        if (endless) {
 #pragma unroll
-        for (int k = 8; k > 0; k >>= 1) {
-            const float m2 = __shfl_xor_sync(0xffffffffu, cm, k), s2 = __shfl_xor_sync(0xffffffffu, cs, k);
-            join_sum(cm, cs, m2, s2);
+            for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+        } else {
+            join_lanes<32>(m, s);
         }
         if (lane == 0) {
-            *om = cm;
-            *os = endless ? (float)sm.n_tail : cs;
-            *on = n;
+            sm.wm[warp] = m;
+            sm.ws[warp] = s;
         }
+        __syncthreads();
+        joined();
+        if (endless) {
+            cm = INFINITY;
+            cs = 0.f;
+            for (int w = 0; w < W; ++w) cs += sm.ws[w];
+        }
+        m = sm.gmax[tid / GROUP];            // at least this thread's maximum
     }
-    if (n == 0) return;
-    // gather what reaches the bound; where too much does (ties, or the best all in a few groups), only
+    if (tid == 0) {
+        *om = cm;
+        *os = cs;
+    }
+    // gather what reaches the bound; where too much does (ties, or the best all with a few threads), only
     // what is above it; where that is still too much, raise the bound to the n-th of what was gathered
-    bool above = false;
+    bool above = bound == -INFINITY;
     for (;;) {
-        if (m >= bound) {
-            for (int i = begin + 4 * tid; i < end; i += 4 * kBeamThreads) {
-                const float4 v = load4<ALIGNED>(row, i, end);
+        uint32_t hit = __ballot_sync(0xffffffffu, n > 0 && (above ? m > bound : m >= bound));
+        while (hit) {
+            // two owners at once: their tokens by lanes, 128 a round each
+            int owner[2];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float x = (&v.x)[k];
-                    if (i + k < end && (above ? x > bound : x >= bound)) {
-                        const int at = atomicAdd(&sm.n_list, 1);
-                        if (at < kList) sm.list[at] = Cand{x, i + k};
+            for (int o = 0; o < 2; ++o) {
+                owner[o] = hit ? begin + warp * 32 + __ffs(hit) - 1 : end;
+                hit &= hit - 1;
+            }
+            for (int step = lane * T; step < end - begin; step += 128 * T) {
+                float x[2][4];
+#pragma unroll
+                for (int o = 0; o < 2; ++o)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int i = owner[o] + step + u * 32 * T;
+                        x[o][u] = i < end ? __ldg(row + i) : NAN;
                     }
-                }
+#pragma unroll
+                for (int o = 0; o < 2; ++o)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (above ? x[o][u] > bound : x[o][u] >= bound) {
+                            const int at = atomicAdd(&sm.n_list, 1);
+                            if (at < kList) sm.list[at] = Cand{x[o][u], owner[o] + step + u * 32 * T};
+                        }
             }
         }
         __syncthreads();
@@ -226,7 +263,7 @@ __device__ __forceinline__ void scan_piece(BeamSmem& sm, const float* row, int b
         if (found <= kList) break;
         if (above) {
             // the n-th largest value of the list
-            for (int e = tid; e < kList; e += kBeamThreads) {
+            for (int e = tid; e < kList; e += T) {
                 const float x = sm.list[e].x;
                 int more = 0, same = 0;
                 for (int f = 0; f < kList; ++f) {
@@ -249,7 +286,7 @@ __device__ __forceinline__ void scan_piece(BeamSmem& sm, const float* row, int b
         __syncthreads();
         if (tid == 0) sm.n_tail = found;
         __syncthreads();
-        for (int base = begin; base < end; base += kBeamThreads) {
+        for (int base = begin; base < end; base += T) {
             const int have = sm.n_tail;
             if (have >= n) break;
             const int i = base + tid;
@@ -258,7 +295,7 @@ __device__ __forceinline__ void scan_piece(BeamSmem& sm, const float* row, int b
             if (lane == 0) sm.wcount[warp] = __popc(mask);
             __syncthreads();
             int at = have, all = have;
-            for (int w = 0; w < kBeamWarps; ++w) {
+            for (int w = 0; w < W; ++w) {
                 if (w < warp) at += sm.wcount[w];
                 all += sm.wcount[w];
             }
@@ -271,7 +308,7 @@ __device__ __forceinline__ void scan_piece(BeamSmem& sm, const float* row, int b
         found = n;
     }
     // ranked by counting
-    for (int e = tid; e < found; e += kBeamThreads) {
+    for (int e = tid; e < found; e += T) {
         const Cand c = sm.list[e];
         int rank = 0;
         for (int f = 0; f < found; ++f) {
@@ -280,98 +317,136 @@ __device__ __forceinline__ void scan_piece(BeamSmem& sm, const float* row, int b
         }
         if (rank < n) out[rank] = c;
     }
-    __syncthreads();
+    if (tid >= n && tid < want) out[tid] = Cand{-INFINITY, -1};
 }
 
-template <bool ALIGNED>
-__global__ void __launch_bounds__(kBeamThreads) k_beam_select(const __grid_constant__ BeamArgs a) {
+template <int T>
+__global__ void __launch_bounds__(T, 1024 / T) k_beam_select(const __grid_constant__ BeamArgs a) {
     __shared__ BeamSmem sm;
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-    const int b = blockIdx.x / C, tid = threadIdx.x;
+    const int b = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31;
+    cudaGridDependencySynchronize();           // everything enqueued before has run
+    auto running = cluster.barrier_arrive();   // waited for before another CTA's shared memory is written
     BeamSmem* head = cluster.map_shared_rank(&sm, 0);
-    const int pieces = a.beams * a.splits;
-    cluster.sync();                       // every CTA of the cluster runs: its shared memory may be written
+    const int n = min(a.n_out, a.vocab);
+    // the finished beams, as bits; the others' rows are cut into `splits` pieces each, numbered piece by
+    // piece in the order of the beams, then one piece for each finished beam
+    const bool mine = a.finished && lane < a.beams && a.finished[b * a.beams + (lane < a.beams ? lane : 0)] != 0;
+    const uint32_t done = __ballot_sync(0xffffffffu, mine), open = ((1u << a.beams) - 1u) & ~done;
+    const int rows = __popc(open);
+    const int splits = rows ? max(1, min(kMaxPieces - (a.beams - rows), C) / rows) : 1;
+    const int pieces = rows * splits + a.beams - rows;
+    auto beam_of = [&](int p) {          // the beam of piece p
+        uint32_t left = p < rows * splits ? open : done;
+        for (int i = p < rows * splits ? p / splits : p - rows * splits; i > 0; --i) left &= left - 1;
+        return __ffs(left) - 1;
+    };
+    bool waited = false;
     for (int p = rank; p < pieces; p += C) {
-        const int k = p / a.splits, j = p % a.splits;
-        const int begin = min(j * a.piece, a.vocab), end = min(begin + a.piece, a.vocab);
-        if (a.finished && a.finished[b * a.beams + k] != 0) {
-            // eos at no cost, then the lowest other tokens at -infinity; all in the row's first piece
-            const int n = j == 0 ? min(a.n_out, a.vocab) : 0;
+        const int k = beam_of(p);
+        if (p >= rows * splits) {
+            // eos at no cost, then the lowest other tokens at -infinity
+            if (!waited) cluster.barrier_wait(std::move(running));
+            waited = true;
             if (tid < n) {
                 const int other = tid - 1 + (tid - 1 >= a.eos);
                 head->cand[p][tid] = tid == 0 ? Cand{0.f, a.eos} : Cand{-INFINITY, other};
             }
-            if (tid == 0) {
-                head->m[p] = j == 0 ? 0.f : -INFINITY;
-                head->s[p] = j == 0 ? 1.f : 0.f;
-                head->count[p] = n;
-            }
             continue;
         }
+        const int size = (a.vocab + splits - 1) / splits;
+        const int begin = min(p % splits * size, a.vocab), end = min(begin + size, a.vocab);
         const float* row = a.logits + (size_t)(b * a.beams + k) * a.ld;
-        scan_piece<ALIGNED>(sm, row, begin, end, a.n_out, head->cand[p], &head->m[p], &head->s[p], &head->count[p]);
+        if (!waited) cluster.barrier_wait(std::move(running));
+        waited = true;
+        scan_piece<T>(sm, row, begin, end, n, head->cand[p], &head->m[p], &head->s[p]);
         __syncthreads();
     }
+    if (!waited) cluster.barrier_wait(std::move(running));
     cluster.sync();
     if (rank != 0) return;
-    // each row's maximum and log of its sum
-    if (tid < a.beams) {
-        float m = -INFINITY, s = 0.f;
-        for (int j = 0; j < a.splits; ++j) m = fmaxf(m, sm.m[tid * a.splits + j]);
-        const float ref = finite(m);
-        for (int j = 0; j < a.splits; ++j) s = fmaf(sm.s[tid * a.splits + j], e2((finite(sm.m[tid * a.splits + j]) - ref) * kLog2E), s);
-        sm.m_row[tid] = (double)m;
-        sm.log_row[tid] = log((double)s);
-    }
-    __syncthreads();
-    const int slots = pieces * kMaxOut;
-    int total = 0;
-    for (int p = 0; p < pieces; ++p) total += sm.count[p];
-    // compact the candidates: slot e of piece p is number (sum of the counts before p) + e
-    for (int i = tid; i < slots; i += kBeamThreads) {
-        const int p = i / kMaxOut, e = i % kMaxOut;
-        if (e >= sm.count[p]) continue;
-        int at = e;
-        for (int q = 0; q < p; ++q) at += sm.count[q];
-        const Cand c = sm.cand[p][e];
-        const int k = p / a.splits;
-        const double m = sm.m_row[k], score = (double)a.scores[b * a.beams + k];
-        // equal to the maximum (an infinite one included): no distance
-        const double d = (double)c.x == m ? 0.0 : (double)c.x - m;
-        double t = score + (d - sm.log_row[k]);
-        if (a.finished && a.finished[b * a.beams + k] != 0) t = score + (double)c.x;
+    // every candidate's total. A row's maximum and sum are joined from its pieces by each thread for itself.
+    const int total = pieces * n;
+    for (int i = tid; i < total; i += T) {
+        const int p = i / n, k = beam_of(p);
+        const Cand c = sm.cand[p][i % n];
+        const double score = (double)a.scores[b * a.beams + k];
+        double t;
+        if (done >> k & 1) {
+            t = score + (double)c.x;
+        } else {
+            const int p0 = p / splits * splits;
+            float m = -INFINITY, s = 0.f;
+            for (int j = 0; j < splits; ++j) m = fmaxf(m, sm.m[p0 + j]);
+            const float ref = finite(m);
+            for (int j = 0; j < splits; ++j) s = fmaf(sm.s[p0 + j], e2((finite(sm.m[p0 + j]) - ref) * kLog2E), s);
+            // equal to the maximum (an infinite one included): no distance
+            const double d = c.x == m ? 0.0 : (double)c.x - (double)m;
+            t = score + (d - log((double)s));
+        }
         if (c.x == -INFINITY || !(t == t)) t = -INFINITY;
-        sm.total[at] = ordered(t);
-        sm.tie[at] = ((unsigned long long)(kMaxBeams - 1 - k) << 56) | ((unsigned long long)ordered(c.x) << 24) |
-                     (unsigned long long)((1 << 24) - 1 - c.token);
+        Key key{0ull, 0ull};             // below every candidate
+        if (c.token >= 0)
+            key = Key{ordered(t), ((unsigned long long)(kMaxBeams - 1 - k) << 56) | ((unsigned long long)ordered(c.x) << 24) |
+                                      (unsigned long long)((1 << 24) - 1 - c.token)};
+        sm.key[i] = key;
     }
-    __syncthreads();
-    for (int i = tid; i < total; i += kBeamThreads) {
-        const unsigned long long t = sm.total[i], x = sm.tie[i];
+    __syncthreads();                     // every read of the scores precedes the writes (they may be the same array)
+    // a candidate's rank: how many of each piece's list (which is in order) come before it, by search;
+    // as many lanes a candidate as there are
+    int lanes = 1;
+    while (lanes < 16 && 2 * lanes * total <= T) lanes *= 2;
+    for (int base = 0; base < total; base += T / lanes) {
+        const int i = base + tid / lanes;
+        const Key x = sm.key[min(i, total - 1)];
         int r = 0;
-        for (int f = 0; f < total; ++f) {
-            const unsigned long long o = sm.total[f];
-            r += o > t || (o == t && sm.tie[f] > x);
+        for (int q = tid & (lanes - 1); q < pieces; q += lanes) {
+            int lo = 0, hi = n;
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                const Key o = sm.key[q * n + mid];
+                if ((o.total > x.total) | ((o.total == x.total) & (o.tie > x.tie))) lo = mid + 1;
+                else hi = mid;
+            }
+            r += lo;
         }
-        if (r < a.n_out) {
-            const int k = kMaxBeams - 1 - (int)(x >> 56), token = (1 << 24) - 1 - (int)(x & 0xffffffu);
-            const unsigned long long u = t >> 63 ? t & 0x7fffffffffffffffull : ~t;
-            const int fin = a.finished ? (a.finished[b * a.beams + k] != 0 || token == a.eos) : 0;
-            sm.list[r] = Cand{(float)__longlong_as_double((long long)u), token};
-            sm.from[r] = make_int2(b * a.beams + k, fin);
+        for (int k = lanes / 2; k > 0; k >>= 1) r += __shfl_xor_sync(0xffffffffu, r, k);
+        if (i < total && (tid & (lanes - 1)) == 0 && r < a.n_out && x.tie != 0ull) {
+            const size_t o = (size_t)b * a.n_out + r;
+            const int k = kMaxBeams - 1 - (int)(x.tie >> 56), token = (1 << 24) - 1 - (int)(x.tie & 0xffffffu);
+            const unsigned long long u = x.total >> 63 ? x.total & 0x7fffffffffffffffull : ~x.total;
+            a.next_tokens[o] = token;
+            a.parents[o] = b * a.beams + k;
+            a.next_scores[o] = (float)__longlong_as_double((long long)u);
+            if (a.next_finished) a.next_finished[o] = (done >> k & 1) || token == a.eos;
         }
-    }
-    __syncthreads();                      // every read of scores and finished precedes the writes (they may be the same arrays)
-    if (tid < a.n_out) {
-        const size_t o = (size_t)b * a.n_out + tid;
-        const int2 pf = sm.from[tid];
-        a.next_tokens[o] = sm.list[tid].token;
-        a.parents[o] = pf.x;
-        a.next_scores[o] = sm.list[tid].x;
-        if (a.next_finished) a.next_finished[o] = pf.y;
     }
     if (a.positions && tid < a.beams) a.positions[b * a.beams + tid] += 1;
+}
+
+template <int T>
+cudaError_t launch_beam(const BeamArgs& a, int C, cudaStream_t st) {
+    static std::atomic<uint64_t> seen{0};
+    if (first_on_device(seen)) {
+        const cudaError_t e = cudaFuncSetAttribute(k_beam_select<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        seen_on_device(seen);
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(a.batch * C));
+    cfg.blockDim = dim3(T);
+    cfg.stream = st;
+    cudaLaunchAttribute at[2]{};
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)C;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    // placed while the kernel before it ends; it waits for all of that before it reads or writes
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_beam_select<T>, a);
 }
 
 }  // namespace
@@ -403,23 +478,18 @@ extern "C" mk_status mk_beam_select(const float* logits, int64_t row_stride, int
     a.next_scores = next_scores;
     a.next_finished = next_finished;
     a.positions = positions;
-    int C = mk::kMaxCluster;
-    while (C > 1 && (long long)batch * C > 2 * mk::kQSms) C /= 2;
-    a.splits = C / beams > 1 ? C / beams : 1;
-    a.piece = ((vocab + a.splits - 1) / a.splits + 3) / 4 * 4;
-    if (C > beams * a.splits) C = beams * a.splits;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(batch * C));
-    cfg.blockDim = dim3(mk::kBeamThreads);
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)C;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    const bool aligned = (reinterpret_cast<uintptr_t>(logits) & 15) == 0 && row_stride % 4 == 0;
-    const cudaError_t e = aligned ? cudaLaunchKernelEx(&cfg, mk::k_beam_select<true>, static_cast<const mk::BeamArgs>(a))
-                                  : cudaLaunchKernelEx(&cfg, mk::k_beam_select<false>, static_cast<const mk::BeamArgs>(a));
-    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+    // CTAs per sequence. Few sequences with long rows take 16 (2 x 4 rows of 128256: 10.0 us against 11.0 with
+    // 8), a moderate number 8 (8 rows of 128256: 7.7 us, 11.4 with 16; 32 x 8 of 50257: 17, 29 with 16), and
+    // from there on a CTA takes whole rows (64 x 4 of 32000: 12.0 us, 20.3 with 8).
+    int C = beams < 8 ? beams : 8;
+    if (batch <= 4 && (int64_t)beams * vocab >= 1 << 18) C = 16;
+    else if (batch <= 32) C = 8;
+    // Threads by the piece's length: long pieces want loads on the way (32 x 4 rows of 128256: 20.4 us with 512,
+    // 23.3 with 256), short ones several CTAs on an SM (512 x 4 rows of 4096: 16.7 us with 128, 30.5 with 256).
+    const int tokens = vocab / (C > beams ? C / beams : 1);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = tokens >= 16384 ? mk::launch_beam<512>(a, C, st)
+                          : tokens >= 6144 ? mk::launch_beam<256>(a, C, st)
+                                           : mk::launch_beam<128>(a, C, st);
+    return e == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }

@@ -760,9 +760,14 @@ template <int HD>
 cudaError_t attn_launch(const AttnArgs& a, cudaStream_t st) {
     const int smem = (int)sizeof(AttnSmem<HD>);
     const bool whole = a.n_cta == 0;
-    const void* f = whole ? (const void*)k_attn_whole<HD> : (const void*)k_attn_split<HD>;
-    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    static std::atomic<uint64_t> seen{0};
+    cudaError_t e = cudaSuccess;
+    if (first_on_device(seen)) {
+        e = cudaFuncSetAttribute(k_attn_whole<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(k_attn_split<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        seen_on_device(seen);
+    }
     if (whole) return launch_behind(k_attn_whole<HD>, a.rows * a.n_heads, 32 * kAttWarps, smem, st, a);
     e = launch_behind(k_attn_split<HD>, a.n_cta, 32 * kAttWarps, smem, st, a);
     if (e != cudaSuccess) return e;

@@ -1,8 +1,11 @@
 // The 8-bit cache's geometry, shared by its kernels and entry points.
 #pragma once
 
+#include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "mk_internal.h"
 
@@ -14,6 +17,18 @@ constexpr int kQSms = 148;        // B200: sizes grids and workspaces without as
 // A block whose largest magnitude is below 2^-60 is held as zeros (scale 0): the
 // attention divides by scales, and 127 / amax has to stay finite.
 constexpr float kQNoBlock = 8.673617379884035e-19f;
+
+// True the first time it is asked on the calling thread's current device (per flag word): for
+// settings of a kernel that last as long as the process. Two threads may both be told so.
+inline bool first_on_device(std::atomic<uint64_t>& seen) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev > 63) return true;
+    return !(seen.load(std::memory_order_acquire) >> dev & 1);
+}
+inline void seen_on_device(std::atomic<uint64_t>& seen) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64) seen.fetch_or(1ull << dev, std::memory_order_release);
+}
 
 inline int qcache_blocks(int max_seq) { return (max_seq + kQBlock - 1) / kQBlock; }
 

@@ -37,7 +37,12 @@ def _at(t: torch.Tensor, dtype: torch.dtype, n: int, device: int) -> int:
 
 
 def _raw_stream(stream, device: int) -> int:
-    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
+# The current device of a thread that already holds CUDA tensors (torch.cuda.current_device without its
+# initialisation check, which costs as much as a launch).
+_current_device = torch._C._cuda_getDevice
 
 
 class Megakernel:
@@ -138,7 +143,7 @@ class Megakernel:
         """One step as ordinary kernels on an 8-bit cache (``qcache.QCache``); it needs no schedule, and
         contexts may be as long as the cache. ``status`` (int32 [1], optional) receives the step's
         device status. Without a ``workspace`` one is allocated for the call."""
-        device = torch.cuda.current_device()
+        device = _current_device()
         batch = tokens.numel()
         max_ctx = min(cache.max_seq, self.max_seq) if max_ctx is None else max_ctx
         if workspace is None:
@@ -252,7 +257,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, next_tokens: torch.T
     ``eos`` at its own score; ``next_finished`` receives who is finished then. ``positions``
     (optional, one per row) are advanced by one. ``next_scores`` may be ``scores`` and
     ``next_finished`` may be ``finished``."""
-    device = torch.cuda.current_device()
+    device = _current_device()
     rows, vocab = logits.shape
     batch, beams = scores.shape
     out_batch, n_out = next_tokens.shape
@@ -276,7 +281,7 @@ def cache_reorder(k_cache: torch.Tensor, v_cache: torch.Tensor, parents: torch.T
     starts[r] .. lengths[parents[r]] - 1, all rows at once and in place, asynchronous on ``stream``: beams
     that follow ``beam_select``, a sequence forked into free rows, live rows moved over finished ones.
     A parent that is the row itself or no row (-1) leaves the row as it is."""
-    device = torch.cuda.current_device()
+    device = _current_device()
     rows = parents.numel()
     n_layers, max_batch, heads, max_seq, dim = k_cache.shape
     assert v_cache.shape == k_cache.shape

@@ -15,7 +15,7 @@ import torch
 
 from . import _lib
 from .config import ModelConfig
-from .model import _at, _raw_stream
+from .model import _at, _current_device, _raw_stream
 
 BLOCK = _lib.QCACHE_BLOCK
 _Strides = ctypes.c_int64 * 4
@@ -65,7 +65,7 @@ class QCache:
         """Stores ``k`` and ``v`` (bf16 [layers][rows][heads][tokens][dim], any strides with the dims
         contiguous) from slot ``positions[row]`` on: ``counts[row]`` tokens of each row (all of them
         where ``counts`` is None), in layers ``first_layer`` on."""
-        device = torch.cuda.current_device()
+        device = _current_device()
         layers, rows, heads, tokens, dim = shape = k.shape
         strides = k.stride()
         assert v.shape == shape and heads == self.n_kv_heads and dim == self.head_dim and strides[4] == 1
@@ -81,7 +81,7 @@ class QCache:
 
     def reorder(self, parents, lengths, starts=None, stream=None) -> None:
         """Row r takes over row parents[r]'s slots starts[r] .. lengths[parents[r]] - 1, all rows at once."""
-        device = torch.cuda.current_device()
+        device = _current_device()
         rows = parents.numel()
         assert self._device == device
         _lib.check(_lib.lib().mk_qcache_reorder(
@@ -99,7 +99,7 @@ class QCache:
         """out[row][head] = attention of q[row][head] (fp32 [rows][n_heads][dim]) over slots
         0 .. positions[row] of ``layer``; a negative position gives zeros. ``max_ctx``: no row has more
         slots (max_seq where None). Without a ``workspace`` one is allocated for the call."""
-        device = torch.cuda.current_device()
+        device = _current_device()
         rows, n_heads, dim = q.shape
         n = rows * n_heads * dim
         assert dim == self.head_dim and self._device == device
