@@ -30,6 +30,25 @@ inline void seen_on_device(std::atomic<uint64_t>& seen) {
     if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64) seen.fetch_or(1ull << dev, std::memory_order_release);
 }
 
+#ifdef __CUDACC__
+// A kernel that may be placed while the one before it in the stream still ends; each waits for
+// all of it (cudaGridDependencySynchronize) before it reads or writes anything.
+template <class... P, class... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int block, int smem, cudaStream_t st, A&&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+#endif
+
 inline int qcache_blocks(int max_seq) { return (max_seq + kQBlock - 1) / kQBlock; }
 
 // MK_OK, or why the cache described by c is refused.

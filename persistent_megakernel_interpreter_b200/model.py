@@ -12,6 +12,7 @@ PyTorch supplies device memory and streams only.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -275,6 +276,12 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, next_tokens: torch.T
         "mk_beam_select")
 
 
+@functools.lru_cache(maxsize=64)
+def _cache_shape(n_layers: int, max_batch: int, heads: int, max_seq: int, dim: int):
+    """The part of a config that says how a cache is laid out, as an argument."""
+    return ctypes.byref(_lib.MkConfig(n_layers, 0, 0, heads, dim, 0, 0, 0.0, 0.0, max_batch, max_seq))
+
+
 def cache_reorder(k_cache: torch.Tensor, v_cache: torch.Tensor, parents: torch.Tensor, lengths: torch.Tensor,
                   starts=None, stream=None) -> None:
     """Row r of both caches (bf16 [layers][rows][heads][max_seq][dim]) takes over row parents[r]'s slots
@@ -285,9 +292,8 @@ def cache_reorder(k_cache: torch.Tensor, v_cache: torch.Tensor, parents: torch.T
     rows = parents.numel()
     n_layers, max_batch, heads, max_seq, dim = k_cache.shape
     assert v_cache.shape == k_cache.shape
-    cfg = _lib.MkConfig(n_layers, 0, 0, heads, dim, 0, 0, 0.0, 0.0, max_batch, max_seq)
     _lib.check(_lib.lib().mk_cache_reorder(
-        ctypes.byref(cfg), _at(k_cache, torch.bfloat16, 1, device), _at(v_cache, torch.bfloat16, 1, device), rows,
+        _cache_shape(n_layers, max_batch, heads, max_seq, dim), _at(k_cache, torch.bfloat16, 1, device), _at(v_cache, torch.bfloat16, 1, device), rows,
         _at(parents, torch.int32, rows, device), _at(lengths, torch.int32, rows, device),
         None if starts is None else _at(starts, torch.int32, rows, device), _raw_stream(stream, device)),
         "mk_cache_reorder")

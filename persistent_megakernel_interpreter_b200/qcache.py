@@ -71,10 +71,12 @@ class QCache:
         assert v.shape == shape and heads == self.n_kv_heads and dim == self.head_dim and strides[4] == 1
         assert k.dtype is torch.bfloat16 and v.dtype is torch.bfloat16
         assert k.get_device() == device and v.get_device() == device and self._device == device
-        strides = [s if n > 1 else 0 for s, n in zip(strides, shape)]
-        assert v.stride() == k.stride() or strides == [s if n > 1 else 0 for s, n in zip(v.stride(), shape)]
+        if v.stride() != strides or (strides[0] | strides[1] | strides[2] | strides[3]) & 7:
+            # the stride of a dimension of one is any number
+            strides = [s if n > 1 else 0 for s, n in zip(strides, shape)]
+            assert strides == [s if n > 1 else 0 for s, n in zip(v.stride(), shape)]
         _lib.check(_lib.lib().mk_qcache_append(
-            self._ref, first_layer, layers, rows, tokens, k.data_ptr(), v.data_ptr(), _Strides(*strides[:4]),
+            self._ref, first_layer, layers, rows, tokens, k.data_ptr(), v.data_ptr(), _Strides(strides[0], strides[1], strides[2], strides[3]),
             _at(positions, torch.int32, rows, device),
             None if counts is None else _at(counts, torch.int32, rows, device), _raw_stream(stream, device)),
             "mk_qcache_append")
