@@ -299,6 +299,7 @@ __device__ __forceinline__ void attn_blocks(const AttnArgs& a, AttnSmem<HD>& sm,
     // + 0 .. 7 behind (HD / 4) t.
     uint32_t qa[2 * C][4];
     float kmul;
+    const uint32_t sel_q = up ? 0x5140u : 0x7362u;   // (lower, lower, upper, upper) digits of two elements
     {
         float big = 0.f;
         bool bad = false;
@@ -321,21 +322,17 @@ __device__ __forceinline__ void attn_blocks(const AttnArgs& a, AttnSmem<HD>& sm,
         for (int j = 0; j < 2 * C; ++j)
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-                uint32_t hi = 0, lo = 0;
+                // x = sum of d_i 256^i with d_i in -128 .. 127: the bytes of x + 0x808080 are d_i + 128 but
+                // for the top one, and d_i itself once the added bits are flipped
+                uint32_t x[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    int x = head < a.group ? __float2int_rn(q[16 * (j / 2) + 8 * (j % 2) + 4 * w + e] * step) : 0;
-                    int d[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        d[i] = (int)(signed char)(x & 255);
-                        x = (x - d[i]) >> 8;
-                    }
-                    hi |= (uint32_t)((up ? d[1] : d[3]) & 255) << (8 * e);
-                    lo |= (uint32_t)((up ? d[0] : d[2]) & 255) << (8 * e);
+                    const int v = head < a.group ? __float2int_rn(q[16 * (j / 2) + 8 * (j % 2) + 4 * w + e] * step) : 0;
+                    x[e] = ((uint32_t)v + 0x808080u) ^ 0x808080u;
                 }
-                qa[j][2 * w] = hi;
-                qa[j][2 * w + 1] = lo;
+                const uint32_t p = __byte_perm(x[0], x[1], sel_q), r = __byte_perm(x[2], x[3], sel_q);
+                qa[j][2 * w] = __byte_perm(p, r, 0x7632);
+                qa[j][2 * w + 1] = __byte_perm(p, r, 0x5410);
             }
     }
     const float sm0 = up ? 256.0f : 16777216.0f, sm1 = up ? 1.0f : 65536.0f;       // a score's digits
@@ -547,28 +544,32 @@ __device__ __forceinline__ void attn_tail(const AttnArgs& a, AttnSmem<HD>& sm, s
 template <int HD, bool FINAL>
 __device__ __forceinline__ void attn_join(const AttnArgs& a, AttnSmem<HD>& sm, uint32_t parts, float* o, float* ml) {
     __syncthreads();
-    for (int e = threadIdx.x; e < a.group * HD; e += 32 * kAttWarps) {
-        const int h = e / HD, d = e % HD;
-        float M = -INFINITY;
+    constexpr int QE = kMaxGroupHeads * HD / (32 * kAttWarps);
 #pragma unroll
-        for (int p = 0; p <= kAttWarps; ++p)
-            if (parts >> p & 1) M = fmaxf(M, sm.m[p][h]);
-        float l = 0.f, x = 0.f;
+    for (int i = 0; i < QE; ++i) {
+        const int e = i * 32 * kAttWarps + (int)threadIdx.x, h = e / HD, d = e % HD;
+        if (h >= a.group) break;
+        float m[kAttWarps + 1], x[kAttWarps + 1], ls[kAttWarps + 1], M = -INFINITY;
 #pragma unroll
-        for (int p = 0; p <= kAttWarps; ++p)
-            if (parts >> p & 1) {
-                const float f = exp2f(sm.m[p][h] - M);
-                l = fmaf(f, sm.l[p][h], l);
-                x = fmaf(f, sm.o(p, h)[d], x);
-            }
+        for (int p = 0; p <= kAttWarps; ++p) {
+            const bool there = parts >> p & 1;
+            m[p] = there ? sm.m[p][h] : -INFINITY;
+            ls[p] = there ? sm.l[p][h] : 0.f;
+            x[p] = there ? sm.o(p, h)[d] : 0.f;
+            M = fmaxf(M, m[p]);
+        }
+        float l = 0.f, y = 0.f;
+#pragma unroll
+        for (int p = 0; p <= kAttWarps; ++p) {
+            const float f = ex2(m[p] - M);
+            l = fmaf(f, ls[p], l);
+            y = fmaf(f, x[p], y);
+        }
         if (FINAL) {
-            o[e] = x / l;
+            o[e] = y / l;
         } else {
-            o[e] = x;
-            if (d == 0) {
-                ml[2 * h] = M;
-                ml[2 * h + 1] = l;
-            }
+            o[e] = y;
+            if (d == 0) *reinterpret_cast<float2*>(ml + 2 * h) = make_float2(M, l);
         }
     }
     __syncthreads();
@@ -580,44 +581,56 @@ __device__ __forceinline__ AttnSmem<HD>& attn_smem() {
     return *reinterpret_cast<AttnSmem<HD>*>(attn_raw);
 }
 
-template <int HD>
-__device__ __forceinline__ void attn_load_q(const AttnArgs& a, AttnSmem<HD>& sm, int b, int h) {
-    const float* q = a.q + ((size_t)b * a.n_heads + h) * a.group * HD;
-    for (int e = threadIdx.x; e < a.group * HD; e += 32 * kAttWarps) (&sm.q[0][0])[e] = q[e];
-    __syncthreads();
-}
-
 __device__ __forceinline__ int attn_keys(const AttnArgs& a, int b) {
     const int pos = a.positions[b];
     return pos >= a.max_ctx ? a.max_ctx : max(pos, -1) + 1;
 }
 
-__device__ __forceinline__ int attn_units(const AttnArgs& a, int b) { return (attn_keys(a, b) + kQBlock - 1) / kQBlock; }
-// A (row, KV head)'s share of the order: its blocks behind kPad units without work, which stand for what
-// starting and joining one more piece (its open block among it) costs the CTA that has them. 0 / 8 /
-// 16 / 24 / 32 units: 61.1 / 58.8 / 57.0 / 56.4 / 56.4 us at 4 x 60001 keys of 128 dims.
+// The order in which the split deals out blocks: row by row, head by head, each (row, KV head) with its
+// blocks (the open one included) behind kPad units without work, which stand for what starting and
+// joining one more piece costs the CTA that has them. 0 / 8 / 16 / 24 / 32 units: 61.1 / 58.8 / 57.0 /
+// 56.4 / 56.4 us at 4 x 60001 keys of 128 dims.
 constexpr int kPad = 24;
-__device__ __forceinline__ int attn_share(const AttnArgs& a, int b) {
-    const int n = attn_units(a, b);
-    return n ? n + kPad : 0;
-}
+__device__ __forceinline__ int attn_units(int keys) { return (keys + kQBlock - 1) / kQBlock; }
+__device__ __forceinline__ int attn_share(int keys) { return keys ? attn_units(keys) + kPad : 0; }
 
-// How the blocks (open ones included) of all rows and KV heads, in that order, are cut over
-// the CTAs of the split: `units` blocks over `n` CTAs, CTA c taking [c units / n,
-// (c + 1) units / n).
-struct SplitPlan {
-    int units, n;
-    __device__ __forceinline__ int start(int c) const { return (int)((long long)c * units / n); }
-    __device__ __forceinline__ int owner(int u) const { return (int)(((long long)(u + 1) * n - 1) / units); }
-};
+// `units` over `n` CTAs, in order: the first `more` CTAs take each + 1 of them, the others `each`.
 template <int HD>
-__device__ __forceinline__ SplitPlan split_plan(const AttnArgs& a) {
-    SplitPlan p{0, 0};
-    for (int b = 0; b < a.rows; ++b) p.units += attn_share(a, b) * a.n_heads;
-    constexpr int least = kAttWarps * batch_blocks(HD);   // a batch for each warp
-    p.n = min(a.n_cta, (p.units + least - 1) / least);
-    return p;
-}
+struct SplitPlan {
+    int keys[kMaxBatch];                 // of each row
+    int n, each, more;
+    __device__ __forceinline__ explicit SplitPlan(const AttnArgs& a) {
+        int units = 0;
+#pragma unroll
+        for (int b = 0; b < kMaxBatch; ++b) keys[b] = b < a.rows ? attn_keys(a, b) : 0;
+#pragma unroll
+        for (int b = 0; b < kMaxBatch; ++b) units += attn_share(keys[b]) * a.n_heads;
+        constexpr int least = kAttWarps * batch_blocks(HD);   // a batch for each warp
+        n = min(a.n_cta, (units + least - 1) / least);
+        each = n ? units / n : 0;
+        more = units - n * each;
+    }
+    __device__ __forceinline__ int start(int c) const { return c * each + min(c, more); }
+    __device__ __forceinline__ int owner(int u) const {
+        const int big = more * (each + 1);
+        return u < big ? u / (each + 1) : more + (u - big) / each;
+    }
+    // The row of unit u, its keys and its first unit.
+    __device__ __forceinline__ void row_of(int u, int n_heads, int& row, int& row_keys, int& first) const {
+        int at = 0;
+        row = row_keys = first = 0;
+#pragma unroll
+        for (int b = 0; b < kMaxBatch; ++b) {
+            const int next = at + attn_share(keys[b]) * n_heads;
+            if (u >= at && u < next) {
+                row = b;
+                row_keys = keys[b];
+                first = at;
+            }
+            at = next;
+        }
+    }
+};
 
 // Blocks [u, stop) of one (row, KV head) with `keys` keys, the open one included, into the
 // parts of sm: which, as bits.
@@ -627,8 +640,19 @@ __device__ __forceinline__ uint32_t attn_range(const AttnArgs& a, AttnSmem<HD>& 
     const size_t plane = ((size_t)a.layer * a.max_batch + b) * a.n_heads + h;
     const int nb = keys / kQBlock;
     const AttnSource<HD> src(a, plane, u, min(stop, nb));
+    // the queries' loads go out ahead of the many of the first batches
+    constexpr int QE = kMaxGroupHeads * HD / (32 * kAttWarps);
+    const float* q = a.q + ((size_t)b * a.n_heads + h) * a.group * HD;
+    float qv[QE];
+#pragma unroll
+    for (int i = 0; i < QE; ++i) {
+        const int e = i * 32 * kAttWarps + (int)threadIdx.x;
+        qv[i] = e < a.group * HD ? q[e] : 0.f;
+    }
     src.start(sm, warp, lane);
-    attn_load_q(a, sm, b, h);
+#pragma unroll
+    for (int i = 0; i < QE; ++i) (&sm.q[0][0])[i * 32 * kAttWarps + threadIdx.x] = qv[i];
+    __syncthreads();
     uint32_t parts = 0;
     if (stop > nb) {
         attn_tail<HD>(a, sm, plane, keys - nb * kQBlock, warp, lane);
@@ -653,46 +677,42 @@ __global__ void __launch_bounds__(32 * kAttWarps, attn_per_sm(HD)) k_attn_whole(
         for (int e = threadIdx.x; e < a.group * HD; e += 32 * kAttWarps) out[e] = 0.f;
         return;
     }
-    const uint32_t parts = attn_range<HD>(a, sm, b, h, 0, attn_units(a, b), keys);
+    const uint32_t parts = attn_range<HD>(a, sm, b, h, 0, attn_units(keys), keys);
     attn_join<HD, true>(a, sm, parts, out, nullptr);
 }
 
-// The split: CTA c takes its range of blocks, which may cover several (row, KV head)
+// The split: CTA c takes its range of the order, which may cover several (row, KV head)
 // pairs; each piece becomes partial slot c + pair (distinct: both only grow along the
-// order of the blocks).
+// order).
 template <int HD>
 __global__ void __launch_bounds__(32 * kAttWarps, attn_per_sm(HD)) k_attn_split(const __grid_constant__ AttnArgs a) {
     AttnSmem<HD>& sm = attn_smem<HD>();
-    // once every CTA runs, the joining kernel may be placed where CTAs end; it waits for them all
-    cudaTriggerProgrammaticLaunchCompletion();
     cudaGridDependencySynchronize();     // everything enqueued before has run
-    const SplitPlan P = split_plan<HD>(a);
+    // once every CTA runs, the joining kernel may be placed where CTAs end; what it reads before it waits for
+    // them (the positions) has been written by then
+    cudaTriggerProgrammaticLaunchCompletion();
+    const SplitPlan<HD> P(a);
     const int c = blockIdx.x;
-    if (c < P.n) {
-        const int u0 = P.start(c), u1 = P.start(c + 1);
-        int first = 0;   // first unit of row b
-        for (int b = 0; b < a.rows && first < u1; ++b) {
-            const int keys = attn_keys(a, b), share = attn_share(a, b);
-            const int last = first + share * a.n_heads;
-            for (int u = max(u0, first); u < min(u1, last);) {
-                const int h = (u - first) / share, base = first + h * share;
-                const int end = min(u1, base + share);
-                // without the padding; a piece of nothing but padding is no piece
-                const int from = max(u - base - kPad, 0), stop = end - base - kPad;
-                if (stop > from) {
-                    const uint32_t parts = attn_range<HD>(a, sm, b, h, from, stop, keys);
-                    const size_t slot = (size_t)c + b * a.n_heads + h;
-                    attn_join<HD, false>(a, sm, parts, a.part_o + slot * a.group * HD, a.part_ml + slot * a.group * 2);
-                }
-                u = end;
-            }
-            first = last;
+    if (c >= P.n) return;
+    const int u1 = P.start(c + 1);
+    for (int u = P.start(c); u < u1;) {
+        int b, keys, first;
+        P.row_of(u, a.n_heads, b, keys, first);
+        const int share = attn_share(keys), h = (u - first) / share, base = first + h * share;
+        const int end = min(u1, base + share);
+        // without the padding; a piece of nothing but padding is no piece
+        const int from = max(u - base - kPad, 0), stop = end - base - kPad;
+        if (stop > from) {
+            const uint32_t parts = attn_range<HD>(a, sm, b, h, from, stop, keys);
+            const size_t slot = (size_t)c + b * a.n_heads + h;
+            attn_join<HD, false>(a, sm, parts, a.part_o + slot * a.group * HD, a.part_ml + slot * a.group * 2);
         }
+        u = end;
     }
 }
 
 // Joins the partials of one (row, query head): warps take slots in turn, lanes the dims.
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 8, kJoinEach = 4;
 template <int HD>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_merge_q(const __grid_constant__ AttnArgs a) {
     constexpr int D = HD / 32;
@@ -700,25 +720,52 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_merge_q(const __grid_c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int heads = a.n_heads * a.group, b = blockIdx.x / heads, hq = blockIdx.x % heads;
     const int h = hq / a.group, hg = hq % a.group, pair = b * a.n_heads + h;
-    const int share = attn_share(a, b);
-    const SplitPlan P = split_plan<HD>(a);
-    int first = 0;
-    for (int i = 0; i < b; ++i) first += attn_share(a, i) * a.n_heads;
+    const SplitPlan<HD> P(a);
+    int first = 0, keys = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxBatch; ++i) {
+        if (i < b) first += attn_share(P.keys[i]) * a.n_heads;
+        if (i == b) keys = P.keys[i];
+    }
+    const int share = attn_share(keys);
     first += h * share;
     const int c0 = share ? P.owner(first + kPad) : 0, total = share ? P.owner(first + share - 1) - c0 + 1 : 0;
     cudaGridDependencySynchronize();
+    // kJoinEach partials of a warp at once, every load issued before the first is used
     float M = -INFINITY, l = 0.f, o[D];
 #pragma unroll
     for (int d = 0; d < D; ++d) o[d] = 0.f;
-    for (int i = warp; i < total; i += kJoinWarps) {
-        const size_t slot = (size_t)c0 + i + pair;
-        const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (slot * a.group + hg) * 2);
-        const float* p = a.part_o + (slot * a.group + hg) * HD + lane * D;
-        const float Mn = fmaxf(M, ml.x), f = exp2f(M - Mn), w = exp2f(ml.x - Mn);
-        M = Mn;
-        l = fmaf(l, f, ml.y * w);
+    for (int i = warp * kJoinEach; i < total; i += kJoinWarps * kJoinEach) {
+        float2 ml[kJoinEach];
+        float p[kJoinEach][D];
 #pragma unroll
-        for (int d = 0; d < D; ++d) o[d] = fmaf(o[d], f, p[d] * w);
+        for (int k = 0; k < kJoinEach; ++k) {
+            const size_t at = ((size_t)c0 + min(i + k, total - 1) + pair) * a.group + hg;
+            ml[k] = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+            if constexpr (D == 2) {
+                const float2 x = *reinterpret_cast<const float2*>(a.part_o + at * HD + lane * D);
+                p[k][0] = x.x; p[k][1] = x.y;
+            } else {
+                const float4 x = *reinterpret_cast<const float4*>(a.part_o + at * HD + lane * D);
+                p[k][0] = x.x; p[k][1] = x.y; p[k][2] = x.z; p[k][3] = x.w;
+            }
+            if (i + k >= total) ml[k] = make_float2(-INFINITY, 0.f);   // a partial's maximum is never below -1e30
+        }
+        float Mn = M;
+#pragma unroll
+        for (int k = 0; k < kJoinEach; ++k) Mn = fmaxf(Mn, ml[k].x);
+        const float f = exp2f(M - Mn);
+        M = Mn;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < D; ++d) o[d] *= f;
+#pragma unroll
+        for (int k = 0; k < kJoinEach; ++k) {
+            const float w = exp2f(ml[k].x - M);
+            l = fmaf(ml[k].y, w, l);
+#pragma unroll
+            for (int d = 0; d < D; ++d) o[d] = fmaf(p[k][d], w, o[d]);
+        }
     }
 #pragma unroll
     for (int d = 0; d < D; ++d) so[warp][lane * D + d] = o[d];
@@ -734,7 +781,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_merge_q(const __grid_c
         out[e] = 0.f;
         return;
     }
-    const int used = min(total, kJoinWarps);
+    const int used = min((total + kJoinEach - 1) / kJoinEach, kJoinWarps);
     float top = -INFINITY, L = 0.f, x = 0.f;
     for (int i = 0; i < used; ++i) top = fmaxf(top, sm[i]);
     for (int i = 0; i < used; ++i) {
@@ -747,9 +794,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_merge_q(const __grid_c
 
 // ------------------------------------------------------------------ launches
 
-constexpr int kWholeCtx = 512;    // contexts up to here run one CTA per (row, head)
-
-bool attn_is_split(int max_ctx) { return max_ctx > kWholeCtx; }
+// One CTA per (row, KV head) up to these contexts, in one kernel; beyond, the split and its joining kernel.
+// With 8 pairs the two take 5.1 and 5.3 us at 1024 keys of 64 dims, 7.6 and 5.4 at 2048; 6.9 and 7.7 at 512 keys of
+// 128, 9.4 and 7.7 at 1024. With 64 pairs 7.8 and 9.5 us at 2048 keys of 64 dims, 13.0 and 11.4 at 4096;
+// 14.7 and 17.2 at 2048 of 128, 28 and 21 at 4096.
+bool attn_is_split(int hd, int pairs, int max_ctx) { return max_ctx > (pairs >= 32 ? 2048 : 65536 / hd); }
+// Floats of the partials' maxima and sums; the outputs behind them are read 16 bytes at a time.
+size_t attn_ml_floats(size_t slots) { return (2 * slots + 3) / 4 * 4; }
 int attn_ctas(int hd) { return kQSms * attn_per_sm(hd); }
 size_t attn_slots(int hd, int rows, int n_heads) { return (size_t)attn_ctas(hd) + (size_t)rows * n_heads; }
 
@@ -821,10 +872,10 @@ extern "C" mk_status mk_qcache_append(const mk_qcache* c, int first_layer, int n
 extern "C" size_t mk_qcache_attention_workspace(const mk_qcache* c, int rows, int n_heads, int max_ctx) {
     if (mk::qcache_check(c) != MK_OK || rows < 1 || rows > c->max_batch || n_heads < c->n_kv_heads ||
         n_heads % c->n_kv_heads != 0 || n_heads / c->n_kv_heads > mk::kMaxGroupHeads || max_ctx < 1 ||
-        max_ctx > c->max_seq || !mk::attn_is_split(max_ctx))
+        max_ctx > c->max_seq || !mk::attn_is_split(c->head_dim, rows * c->n_kv_heads, max_ctx))
         return 0;
     const size_t slots = mk::attn_slots(c->head_dim, rows, c->n_kv_heads) * (size_t)(n_heads / c->n_kv_heads);
-    return slots * (size_t)(c->head_dim + 2) * sizeof(float);
+    return (mk::attn_ml_floats(slots) + slots * (size_t)c->head_dim) * sizeof(float);
 }
 
 extern "C" mk_status mk_qcache_attention(const mk_qcache* c, int layer, int rows, int n_heads, int max_ctx,
@@ -860,7 +911,7 @@ extern "C" mk_status mk_qcache_attention(const mk_qcache* c, int layer, int rows
     if (need) {
         a.n_cta = mk::attn_ctas(c->head_dim);
         a.part_ml = static_cast<float*>(workspace);
-        a.part_o = a.part_ml + mk::attn_slots(c->head_dim, rows, c->n_kv_heads) * (size_t)a.group * 2;
+        a.part_o = a.part_ml + mk::attn_ml_floats(mk::attn_slots(c->head_dim, rows, c->n_kv_heads) * (size_t)a.group);
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = c->head_dim == 64 ? mk::attn_launch<64>(a, st) : mk::attn_launch<128>(a, st);
