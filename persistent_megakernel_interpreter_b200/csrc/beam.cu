@@ -16,7 +16,7 @@
 //   2. of the threads whose maximum reaches it (about n), each one's tokens are read again by its whole
 //      warp at once, and what reaches the bound (about n) is gathered and ranked by counting.
 // Each piece's maximum, sum and candidates go to CTA 0's shared memory (distributed
-// shared memory), which ranks them all by total and writes the answer.
+// shared memory), where one warp merges the ordered lists by total and writes the answer.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -66,6 +66,7 @@ struct BeamSmem {
     // CTA 0's: what every piece found
     Cand cand[kMaxPieces][kMaxOut];
     float m[kMaxPieces], s[kMaxPieces];
+    float score[kMaxBeams];
     Key key[kMaxPieces * kMaxOut];
     // each CTA's own
     Cand list[kList];
@@ -183,27 +184,18 @@ __device__ __forceinline__ void scan_piece(BeamSmem& sm, const float* row, int b
         sm.ws[warp] = cs;
     }
     if (tid == 0) sm.n_list = 0;
-    __syncthreads();
+    const bool odd = __syncthreads_or(!(s <= kBig));
     float bound = n > 0 ? bound_of(reinterpret_cast<const float4*>(sm.gmax)[lane], n, lane) : INFINITY;
-    auto joined = [&] {
-        cm = lane < W ? sm.wm[lane] : -INFINITY;
-        cs = lane < W ? sm.ws[lane] : 0.f;
-        join_lanes<W>(cm, cs);
-        cm = __shfl_sync(0xffffffffu, cm, 0);
-        cs = __shfl_sync(0xffffffffu, cs, 0);
-    };
-    joined();
-    if (!(cs <= kBig)) {
-        // NaN or infinite logits (every warp sees the same sum): once more without the first, and infinite
-        // ones share the row, so that the sum is their number
+    if (odd) {
+        // NaN or infinite logits: once more without the first, and infinite ones share the row, so that the sum
+        // is their number
+        const float reach = m;               // what the thread's numbers reach, for the gathering
         scan_tokens<T, true>(row, begin, end, m, s);
-        if (cm == INFINITY) {
+        const bool endless = __syncthreads_or(m == INFINITY);
+        if (endless) {
             s = 0.f;
             for (int i = begin + tid; i < end; i += T) s += __ldg(row + i) == INFINITY;
-        }
-        __syncthreads();
-        const bool endless = cm == INFINITY;
-        if (endless) {
+            m = INFINITY;
 #pragma unroll
             for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
         } else {
@@ -213,18 +205,23 @@ __device__ __forceinline__ void scan_piece(BeamSmem& sm, const float* row, int b
             sm.wm[warp] = m;
             sm.ws[warp] = s;
         }
+        m = reach;
         __syncthreads();
-        joined();
-        if (endless) {
-            cm = INFINITY;
-            cs = 0.f;
-            for (int w = 0; w < W; ++w) cs += sm.ws[w];
-        }
-        m = sm.gmax[tid / GROUP];            // at least this thread's maximum
     }
-    if (tid == 0) {
-        *om = cm;
-        *os = cs;
+    if (warp == W - 1) {
+        cm = lane < W ? sm.wm[lane] : -INFINITY;
+        cs = lane < W ? sm.ws[lane] : 0.f;
+        if (__any_sync(0xffffffffu, cm == INFINITY)) {
+            cm = INFINITY;
+#pragma unroll
+            for (int k = W / 2; k > 0; k >>= 1) cs += __shfl_xor_sync(0xffffffffu, cs, k);
+        } else {
+            join_lanes<W>(cm, cs);
+        }
+        if (lane == 0) {
+            *om = cm;
+            *os = cs;
+        }
     }
     // gather what reaches the bound; where too much does (ties, or the best all with a few threads), only
     // what is above it; where that is still too much, raise the bound to the n-th of what was gathered
@@ -342,6 +339,7 @@ __global__ void __launch_bounds__(T, 1024 / T) k_beam_select(const __grid_consta
         for (int i = p < rows * splits ? p / splits : p - rows * splits; i > 0; --i) left &= left - 1;
         return __ffs(left) - 1;
     };
+    if (rank == 0 && tid < a.beams) sm.score[tid] = a.scores[b * a.beams + tid];
     bool waited = false;
     for (int p = rank; p < pieces; p += C) {
         const int k = beam_of(p);
@@ -364,14 +362,15 @@ __global__ void __launch_bounds__(T, 1024 / T) k_beam_select(const __grid_consta
         __syncthreads();
     }
     if (!waited) cluster.barrier_wait(std::move(running));
-    cluster.sync();
-    if (rank != 0) return;
+    auto told = cluster.barrier_arrive();
+    if (rank != 0) return;               // nothing of this CTA is read by others
+    cluster.barrier_wait(std::move(told));
     // every candidate's total. A row's maximum and sum are joined from its pieces by each thread for itself.
     const int total = pieces * n;
     for (int i = tid; i < total; i += T) {
         const int p = i / n, k = beam_of(p);
         const Cand c = sm.cand[p][i % n];
-        const double score = (double)a.scores[b * a.beams + k];
+        const double score = (double)sm.score[k];
         double t;
         if (done >> k & 1) {
             t = score + (double)c.x;
@@ -392,37 +391,43 @@ __global__ void __launch_bounds__(T, 1024 / T) k_beam_select(const __grid_consta
                                       (unsigned long long)((1 << 24) - 1 - c.token)};
         sm.key[i] = key;
     }
-    __syncthreads();                     // every read of the scores precedes the writes (they may be the same array)
-    // a candidate's rank: how many of each piece's list (which is in order) come before it, by search;
-    // as many lanes a candidate as there are
-    int lanes = 1;
-    while (lanes < 16 && 2 * lanes * total <= T) lanes *= 2;
-    for (int base = 0; base < total; base += T / lanes) {
-        const int i = base + tid / lanes;
-        const Key x = sm.key[min(i, total - 1)];
-        int r = 0;
-        for (int q = tid & (lanes - 1); q < pieces; q += lanes) {
-            int lo = 0, hi = n;
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                const Key o = sm.key[q * n + mid];
-                if ((o.total > x.total) | ((o.total == x.total) & (o.tie > x.tie))) lo = mid + 1;
-                else hi = mid;
-            }
-            r += lo;
+    __syncthreads();
+    if (a.positions && tid < a.beams) a.positions[b * a.beams + tid] += 1;
+    if (tid >= 32) return;
+    // the best of the heads of the pieces' ordered lists, n_out times: lane p holds piece p's. The next one
+    // that a list would offer is read while the others are compared.
+    const Key none{0ull, 0ull};
+    Key mine_now = lane < pieces ? sm.key[lane * n] : none, won = none;
+    int used = 0;
+    for (int r = 0; r < a.n_out; ++r) {
+        const Key next = lane < pieces && used + 1 < n ? sm.key[lane * n + used + 1] : none;
+        // the largest (total, tie), 32 bits at a time while more than one lane has it
+        uint32_t left = 0xffffffffu;
+#pragma unroll
+        for (int part = 0; part < 4; ++part) {
+            const unsigned long long word = part < 2 ? mine_now.total : mine_now.tie;
+            const uint32_t v = left >> lane & 1 ? (uint32_t)(part & 1 ? word : word >> 32) : 0u;
+            const uint32_t most = __reduce_max_sync(0xffffffffu, v);
+            left &= __ballot_sync(0xffffffffu, v == most);
+            if (!(left & (left - 1))) break;
         }
-        for (int k = lanes / 2; k > 0; k >>= 1) r += __shfl_xor_sync(0xffffffffu, r, k);
-        if (i < total && (tid & (lanes - 1)) == 0 && r < a.n_out && x.tie != 0ull) {
-            const size_t o = (size_t)b * a.n_out + r;
-            const int k = kMaxBeams - 1 - (int)(x.tie >> 56), token = (1 << 24) - 1 - (int)(x.tie & 0xffffffu);
-            const unsigned long long u = x.total >> 63 ? x.total & 0x7fffffffffffffffull : ~x.total;
-            a.next_tokens[o] = token;
-            a.parents[o] = b * a.beams + k;
-            a.next_scores[o] = (float)__longlong_as_double((long long)u);
-            if (a.next_finished) a.next_finished[o] = (done >> k & 1) || token == a.eos;
+        const int winner = __ffs(left) - 1;
+        const Key best{__shfl_sync(0xffffffffu, mine_now.total, winner), __shfl_sync(0xffffffffu, mine_now.tie, winner)};
+        if (lane == r) won = best;
+        if (lane == winner) {
+            mine_now = next;
+            ++used;
         }
     }
-    if (a.positions && tid < a.beams) a.positions[b * a.beams + tid] += 1;
+    if (lane < a.n_out) {
+        const size_t o = (size_t)b * a.n_out + lane;
+        const int k = kMaxBeams - 1 - (int)(won.tie >> 56), token = (1 << 24) - 1 - (int)(won.tie & 0xffffffu);
+        const unsigned long long u = won.total >> 63 ? won.total & 0x7fffffffffffffffull : ~won.total;
+        a.next_tokens[o] = token;
+        a.parents[o] = b * a.beams + k;
+        a.next_scores[o] = (float)__longlong_as_double((long long)u);
+        if (a.next_finished) a.next_finished[o] = (done >> k & 1) || token == a.eos;
+    }
 }
 
 template <int T>

@@ -171,6 +171,7 @@ class Megakernel:
         from .qcache import QCache
         rows = tokens.numel()
         assert scores.dim() == 2 and scores.numel() == rows
+        assert isinstance(cache, QCache) or self.batch == rows, "the schedule is built for another batch"
         for t in (generated, parents):
             assert t is None or (t.dtype == torch.int32 and t.is_contiguous() and t.numel() >= n_steps * rows)
         s = stream or torch.cuda.current_stream()

@@ -64,6 +64,15 @@ def test_beam_select_against_the_plain_form(batch, beams, n_out, vocab):
     check(x, scores, min(n_out, beams * vocab))
 
 
+@pytest.mark.parametrize("batch, beams, vocab, n_out", [(33, 3, 20011, 6), (5, 1, 128256, 8), (2, 9, 30001, 18), (1, 7, 128256, 14),
+                                                         (3, 13, 1000, 32), (129, 16, 300, 4), (64, 1, 9001, 1)])
+def test_every_way_of_cutting_the_rows(batch, beams, vocab, n_out):
+    x, scores, g = draw(batch, beams, vocab, batch)
+    check(x, scores, n_out)
+    fin = (g.random((batch, beams)) < 0.4).astype(np.int32)
+    check(x, scores, n_out, fin, eos=vocab - 1)
+
+
 @pytest.mark.parametrize("offset, stride", [(0, 1004), (1, 1001), (2, 1003), (3, 1024)])
 def test_rows_of_any_alignment_and_stride(offset, stride):
     x, scores, _ = draw(2, 4, 1001, 5)
@@ -156,6 +165,30 @@ def test_select_captured_and_replayed():
 
 
 # ------------------------------------------------------------------ reordering
+
+def test_reorder_captured_and_replayed_with_other_parents():
+    g = np.random.default_rng(2)
+    shape = (2, 4, 2, 100, 64)
+    k0, v0 = (torch.from_numpy(g.integers(-2 ** 15, 2 ** 15, shape).astype(np.int16)).cuda() for _ in range(2))
+    k, v = k0.clone(), v0.clone()
+    par, n = (torch.zeros(4, dtype=torch.int32, device="cuda") for _ in range(2))
+    par.copy_(torch.tensor([-1, 9, 2, 3]))                   # nobody moves
+    cache_reorder(k.view(torch.bfloat16), v.view(torch.bfloat16), par, n)
+    torch.cuda.synchronize()
+    assert torch.equal(k, k0) and torch.equal(v, v0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache_reorder(k.view(torch.bfloat16), v.view(torch.bfloat16), par, n)
+    for parents, lengths in (([1, 0, 0, 3], [50, 100, 7, 9]), ([3, 3, 3, 3], [100, 1, 1, 64])):
+        k.copy_(k0)
+        v.copy_(v0)
+        par.copy_(torch.tensor(parents))
+        n.copy_(torch.tensor(lengths))
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, old in ((k, k0), (v, v0)):
+            assert np.array_equal(got.cpu().numpy(), reorder(old.cpu().numpy(), parents, lambda p, r: (0, lengths[p])))
+
 
 @pytest.mark.parametrize("layers, rows_of, heads, max_seq, dim", [(2, 4, 2, 160, 64), (1, 8, 8, 77, 128), (3, 1, 1, 5, 64),
                                                                (2, 5, 3, 1030, 64), (28, 8, 2, 33, 128)])

@@ -206,10 +206,54 @@ def test_attention_over_long_contexts(dim, heads, rows, n):
     check_attention(c, 0, q, [n - 1 - 37 * r for r in range(rows)], n)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows, heads, group", [(1, 1, 1), (3, 1, 3), (1, 5, 1), (5, 7, 2)])
+def test_attention_on_either_side_of_its_two_forms(dim, rows, heads, group):
+    """Contexts at the border between one CTA per pair and the split, and one past it; odd numbers of partials."""
+    for max_ctx in (65536 // dim, 65536 // dim + 1, 2048, 2049):
+        lengths = [max(0, max_ctx - 31 * r - r * r) for r in range(rows)]
+        c, g = filled(1, rows, heads, dim, max_ctx, lengths, max_ctx + rows)
+        q = torch.from_numpy(g.standard_normal((rows, heads * group, dim)).astype(np.float32)).cuda()
+        check_attention(c, 0, q, [n - 1 for n in lengths], max_ctx)
+
+
+@pytest.mark.parametrize("max_ctx", [100, 5000])
+def test_rows_that_are_all_empty(max_ctx):
+    c = QCache(shape(1, 2, 64), 3, max_ctx)
+    q, out = torch.randn(3, 4, 64, device="cuda"), torch.full((3, 4, 64), 7.0, device="cuda")
+    c.attention(0, q, i32([-1, -2 ** 31, -7]), out)
+    torch.cuda.synchronize()
+    assert torch.all(out == 0)
+
+
+def test_positions_written_by_the_kernel_just_before():
+    """The attention's kernels are placed while the one before them ends; what that one wrote has to be seen."""
+    for max_ctx in (400, 4000):
+        c, g = filled(1, 2, 2, 64, max_ctx, [max_ctx, max_ctx], 31)
+        q = torch.from_numpy(g.standard_normal((2, 4, 64)).astype(np.float32)).cuda()
+        at = [i32([max_ctx - 1, 40]), i32([33, max_ctx // 2]), i32([max_ctx // 3, -1])]
+        ws = c.attention_workspace(2, 4, max_ctx)
+        want = []
+        for p in at:
+            out = torch.empty(2, 4, 64, device="cuda")
+            c.attention(0, q, p, out, workspace=ws)
+            torch.cuda.synchronize()
+            want.append(out)
+        pos, q2 = at[0].clone(), q.clone()
+        outs = [torch.empty(2, 4, 64, device="cuda") for _ in range(300)]
+        for i, out in enumerate(outs):
+            q2.zero_()
+            q2.copy_(q)
+            pos.copy_(at[i % 3])
+            c.attention(0, q2, pos, out, workspace=ws)
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, want[i % 3]) for i, out in enumerate(outs))
+
+
 def test_attention_reads_no_slot_behind_the_last():
     """Garbage (NaN scales, tails of NaN) behind each row's length, and a position beyond max_ctx."""
     lengths = [70, 64, 33, 0]
-    for max_seq in (200, 1000):
+    for max_seq in (200, 1500):
         c, g = filled(1, 4, 2, 64, max_seq, lengths, 5)
         for r, n in enumerate(lengths):
             for scale, tail in ((c.k_scale, c.k_tail), (c.v_scale, c.v_tail)):
@@ -223,7 +267,7 @@ def test_attention_reads_no_slot_behind_the_last():
     check_attention(c, 0, q, [2 ** 31 - 1, -5], 640)
 
 
-@pytest.mark.parametrize("max_seq", [320, 960])
+@pytest.mark.parametrize("max_seq", [320, 1920])
 def test_attention_with_blocks_of_zeros_and_of_very_different_scales(max_seq):
     rows, g = 3, np.random.default_rng(7)
     c = QCache(shape(1, 2, 64), rows, max_seq)
@@ -245,13 +289,13 @@ def test_attention_with_blocks_of_zeros_and_of_very_different_scales(max_seq):
 
 @pytest.mark.parametrize("scale", [1e-20, 1e6])
 def test_queries_of_any_size(scale):
-    c, g = filled(1, 2, 2, 64, 600, [600, 90], 12, scale=1 / scale if scale > 1 else 1.0)
+    c, g = filled(1, 2, 2, 64, 1600, [1600, 90], 12, scale=1 / scale if scale > 1 else 1.0)
     q = torch.from_numpy(g.standard_normal((2, 8, 64)).astype(np.float32) * np.float32(scale)).cuda()
-    check_attention(c, 0, q, [599, 89], 600)
+    check_attention(c, 0, q, [1599, 89], 1600)
     check_attention(c, 0, torch.zeros_like(q), [599, 89], 600)
 
 
-@pytest.mark.parametrize("max_seq", [300, 900])
+@pytest.mark.parametrize("max_seq", [300, 1900])
 def test_a_bad_block_gives_nan_and_only_to_its_row_and_head(max_seq):
     g = np.random.default_rng(13)
     c = QCache(shape(1, 2, 64), 2, max_seq)
@@ -430,4 +474,38 @@ def test_beam_search_on_the_8_bit_cache():
         assert at // beams == r // beams
         texts.add((r // beams, tuple(text)))
     assert len(texts) == rows
+    mk.close()
+
+
+def test_beam_steps_captured_and_replayed():
+    """A step, the choice and the reorder on the 8-bit cache in one graph, replayed, against the same calls."""
+    rows, beams, steps, past, max_seq = 4, 2, 6, 29, 4000
+    mk = Megakernel(TINY, make_weights(TINY, seed=3).to("cuda"), max_batch=rows, max_seq=max_seq)
+    k, v = make_kv_cache(TINY, rows, 64, past=past, seed=4)
+    ends = []
+    for captured in (False, True):
+        c = QCache(TINY, rows, max_seq)
+        c.append(k.cuda(), v.cuda(), i32([0] * rows), counts=i32([past] * rows))
+        tok = make_tokens(TINY, rows, seed=5).to(torch.int32).cuda()
+        pos, start = i32([past] * rows), i32([past] * rows)
+        sc = torch.zeros(2, beams, device="cuda")
+        fin = torch.zeros(2, beams, dtype=torch.int32, device="cuda")
+        lg = torch.empty(rows, TINY.vocab, device="cuda")
+        ws = mk.decode_step_qcache_workspace(c, rows, max_seq)
+        par = torch.zeros(rows, dtype=torch.int32, device="cuda")
+
+        def step():
+            mk.decode_steps_beam(tok, pos, c, lg, sc, 1, finished=fin, eos=7, starts=start, parents=par, workspace=ws)
+
+        if captured:
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                step()
+            step = graph.replay
+        for _ in range(steps):
+            step()
+        torch.cuda.synchronize()
+        ends.append([t.cpu() for t in (tok, pos, sc, fin, par, lg, c.k_codes, c.v_codes, c.k_scale, c.v_scale, c.k_tail, c.v_tail)])
+    assert all(torch.equal(a, b) for a, b in zip(*ends))
     mk.close()
