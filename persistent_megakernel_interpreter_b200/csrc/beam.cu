@@ -35,6 +35,7 @@ constexpr int kMaxBeams = 16;
 constexpr int kMaxOut = 32;
 constexpr int kMaxPieces = 16;            // pieces of a sequence's rows: rows * splits
 constexpr int kList = 1024;               // gathered logits of a piece
+constexpr int kOwn = 8;                   // tokens a thread reads again by itself
 constexpr int kLoads = 32;                // logits a thread has on the way at once
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kBig = 3.402823466e38f;
@@ -66,7 +67,8 @@ struct BeamSmem {
     // CTA 0's: what every piece found
     Cand cand[kMaxPieces][kMaxOut];
     float m[kMaxPieces], s[kMaxPieces];
-    float score[kMaxBeams];
+    float score[kMaxBeams], m_row[kMaxBeams];
+    double log_row[kMaxBeams];
     Key key[kMaxPieces * kMaxOut];
     // each CTA's own
     Cand list[kList];
@@ -126,10 +128,10 @@ __device__ __forceinline__ float bound_of(float4 v, int n, int lane) {
         return __shfl_sync(0xffffffffu, x, __ffs(__ballot_sync(0xffffffffu, rank == n - 1)) - 1);
     }
     // more are wanted: the n-th of 32 maxima would let many times n through. The n-th largest of all 128, to
-    // 20 bits (rounded down), bit by bit
+    // 16 bits (rounded down), bit by bit
     const uint32_t k[4] = {ordered(v.x), ordered(v.y), ordered(v.z), ordered(v.w)};
     uint32_t t = 0;
-    for (int bit = 31; bit >= 12; --bit) {
+    for (int bit = 31; bit >= 16; --bit) {
         const uint32_t c = t | 1u << bit;
         if ((int)__reduce_add_sync(0xffffffffu, (k[0] >= c) + (k[1] >= c) + (k[2] >= c) + (k[3] >= c)) >= n) t = c;
     }
@@ -227,7 +229,23 @@ __device__ __forceinline__ void scan_piece(BeamSmem& sm, const float* row, int b
     // what is above it; where that is still too much, raise the bound to the n-th of what was gathered
     bool above = bound == -INFINITY;
     for (;;) {
-        uint32_t hit = __ballot_sync(0xffffffffu, n > 0 && (above ? m > bound : m >= bound));
+        const bool mine = n > 0 && (above ? m > bound : m >= bound);
+        uint32_t hit = __ballot_sync(0xffffffffu, mine);
+        if (end - begin <= kOwn * T) {
+            // a short piece: each thread reads its own few again
+            hit = 0;
+            if (mine) {
+                float x[kOwn];
+#pragma unroll
+                for (int u = 0; u < kOwn; ++u) x[u] = begin + tid + u * T < end ? __ldg(row + begin + tid + u * T) : NAN;
+#pragma unroll
+                for (int u = 0; u < kOwn; ++u)
+                    if (above ? x[u] > bound : x[u] >= bound) {
+                        const int at = atomicAdd(&sm.n_list, 1);
+                        if (at < kList) sm.list[at] = Cand{x[u], begin + tid + u * T};
+                    }
+            }
+        }
         while (hit) {
             // two owners at once: their tokens by lanes, 128 a round each
             int owner[2];
@@ -365,7 +383,18 @@ __global__ void __launch_bounds__(T, 1024 / T) k_beam_select(const __grid_consta
     auto told = cluster.barrier_arrive();
     if (rank != 0) return;               // nothing of this CTA is read by others
     cluster.barrier_wait(std::move(told));
-    // every candidate's total. A row's maximum and sum are joined from its pieces by each thread for itself.
+    // each unfinished row's maximum and the logarithm of its sum, joined from its pieces
+    if (tid < rows) {
+        const int k = beam_of(tid * splits), p0 = tid * splits;
+        float m = -INFINITY, s = 0.f;
+        for (int j = 0; j < splits; ++j) m = fmaxf(m, sm.m[p0 + j]);
+        const float ref = finite(m);
+        for (int j = 0; j < splits; ++j) s = fmaf(sm.s[p0 + j], e2((finite(sm.m[p0 + j]) - ref) * kLog2E), s);
+        sm.m_row[k] = m;
+        sm.log_row[k] = log((double)s);
+    }
+    __syncthreads();
+    // every candidate's total
     const int total = pieces * n;
     for (int i = tid; i < total; i += T) {
         const int p = i / n, k = beam_of(p);
@@ -375,14 +404,10 @@ __global__ void __launch_bounds__(T, 1024 / T) k_beam_select(const __grid_consta
         if (done >> k & 1) {
             t = score + (double)c.x;
         } else {
-            const int p0 = p / splits * splits;
-            float m = -INFINITY, s = 0.f;
-            for (int j = 0; j < splits; ++j) m = fmaxf(m, sm.m[p0 + j]);
-            const float ref = finite(m);
-            for (int j = 0; j < splits; ++j) s = fmaf(sm.s[p0 + j], e2((finite(sm.m[p0 + j]) - ref) * kLog2E), s);
             // equal to the maximum (an infinite one included): no distance
+            const float m = sm.m_row[k];
             const double d = c.x == m ? 0.0 : (double)c.x - (double)m;
-            t = score + (d - log((double)s));
+            t = score + (d - sm.log_row[k]);
         }
         if (c.x == -INFINITY || !(t == t)) t = -INFINITY;
         Key key{0ull, 0ull};             // below every candidate
@@ -483,12 +508,14 @@ extern "C" mk_status mk_beam_select(const float* logits, int64_t row_stride, int
     a.next_scores = next_scores;
     a.next_finished = next_finished;
     a.positions = positions;
-    // CTAs per sequence. Few sequences with long rows take 16 (2 x 4 rows of 128256: 10.0 us against 11.0 with
-    // 8), a moderate number 8 (8 rows of 128256: 7.7 us, 11.4 with 16; 32 x 8 of 50257: 17, 29 with 16), and
-    // from there on a CTA takes whole rows (64 x 4 of 32000: 12.0 us, 20.3 with 8).
-    int C = beams < 8 ? beams : 8;
-    if (batch <= 4 && (int64_t)beams * vocab >= 1 << 18) C = 16;
-    else if (batch <= 32) C = 8;
+    // CTAs per sequence. Few sequences with long rows or many beams take 16 (2 x 4 rows of 128256: 9.0 us against 11
+    // with 8); a moderate number at least 8 (8 rows of 128256: 7.7 us, 11.4 with 16; 32 x 8 of 50257: 17,
+    // 29 with 16); from there on a CTA takes a whole row (64 x 4 of 32000: 12.0 us, 20.3 with 8), of many sequences
+    // with many beams two (20 x 12 of 32000: 16.3 us with 12 CTAs, 25.6 with 8; 100 x 16: 80 with 16, 69 with 8).
+    const int most = batch <= 64 ? 16 : 8;
+    int C = beams < most ? beams : most;
+    if (batch <= 4 && (beams > 8 || (int64_t)beams * vocab >= 1 << 18)) C = 16;
+    else if (batch <= 32 && C < 8) C = 8;
     // Threads by the piece's length: long pieces want loads on the way (32 x 4 rows of 128256: 20.4 us with 512,
     // 23.3 with 256), short ones several CTAs on an SM (512 x 4 rows of 4096: 16.7 us with 128, 30.5 with 256).
     const int tokens = vocab / (C > beams ? C / beams : 1);
