@@ -317,8 +317,8 @@ mk_status mk_cache_reorder(const mk_config* cfg, void* k_cache, void* v_cache, i
  * NaN gets a NaN scale: whatever attends to it is NaN. */
 #define MK_QCACHE_BLOCK 32
 
-/* Caller-owned device buffers; nothing in them needs to be initialised. The codes and tails are
- * 16-byte aligned. n_blocks = ceil(max_seq / MK_QCACHE_BLOCK). Accepted: 1..64 layers, max_batch 1..8,
+/* Caller-owned device buffers; nothing in them needs to be initialised, and only the calls below
+ * write them. The codes and tails are 16-byte aligned. n_blocks = ceil(max_seq / MK_QCACHE_BLOCK). Accepted: 1..64 layers, max_batch 1..8,
  * 1..32 KV heads, max_seq 1..2^20, head_dim 64 or 128. */
 typedef struct mk_qcache {
     int32_t n_layers, max_batch, n_kv_heads, max_seq, head_dim, reserved0;
@@ -361,8 +361,9 @@ mk_status mk_qcache_reorder(const mk_qcache* c, int rows, const int32_t* parents
  *   workspace     device, 16-byte aligned, mk_qcache_attention_workspace() bytes; need not be
  *                 initialised, belongs to the call until it has run (calls that overlap on the GPU
  *                 need one each); may be NULL where that is 0
- * fp32 arithmetic to about 2^-22 of each product: the codes are exact in fp16 and the queries and
- * weights enter the tensor cores as two fp16 parts. One or two kernel launches; no allocation,
+ * Both products are exact sums of whole numbers (a head's queries in 30 bits of its largest, the softmax's
+ * weights in 32 bits of the largest so far), scaled and added in fp32; the open block is fp32. A query
+ * head with an infinity or a NaN gives NaN. One or two kernel launches; no allocation,
  * capturable; the same inputs give the same bits. */
 mk_status mk_qcache_attention(const mk_qcache* c, int layer, int rows, int n_heads, int max_ctx, const float* q,
                               const int32_t* positions, float* out, void* workspace, size_t workspace_bytes,

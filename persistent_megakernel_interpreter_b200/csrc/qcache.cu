@@ -39,8 +39,9 @@ __device__ __forceinline__ float bf(uint32_t bits16) { return __uint_as_float(bi
 // full 16-byte pieces. The block that stays open is written by the team of window block 0, after it
 // has read the tail's old tokens.
 //
-// Bound by HBM (2 bytes in, 1 out): small CTAs at 64 registers a thread, 16 layers of four prompts of
-// up to 4001 tokens in 113 us, 93% of the measured copy rate; 145 us with 8 warps and 79 registers.
+// Bound by HBM (2 bytes in, 1 out). Small CTAs at 64 registers a thread: 16 layers of four prompts of
+// up to 4001 tokens (688 MB) in 101 us, 104% of the measured copy rate (145 us with 8 warps a CTA, one warp a
+// block and 79 registers); one token of eight rows in 1.3 us.
 template <int HD>
 __global__ void __launch_bounds__(32 * kAppWarps, 8) k_append(const __grid_constant__ AppendArgs a) {
     constexpr int TEAM = HD / 64, TL = 32 * TEAM, TEAMS = kAppWarps / TEAM;
@@ -152,6 +153,13 @@ __global__ void __launch_bounds__(32 * kAppWarps, 8) k_append(const __grid_const
 // A warp works alone on a batch of 8 KB (64 keys and values of 64 dims, 32 of 128), with
 // a running (M, l, O) of its own, fed by a private ring of asynchronous copies; the warps
 // join at the end.
+//
+// Bound by HBM: 2 * dim bytes a key and KV head. Measured on one B200: 4 rows of up to 60001 keys of 128 dims
+// (308 MB) in 53.4 us, 5.76 TB/s (88% of the measured copy rate); 8 rows of up to 16384 keys of 64 dims (105 MB)
+// in 22.1 us (73%); 129 keys in 3.8 us. Around the stream of bytes there are about 6 us: 1.5 to launch, 0.7
+// for the plan, 1.5 until the first batch is here, 1 to join a CTA's warps, 2 for the joining kernel. As fp16
+// products (codes converted, the other operand in two parts) the same took 32 and 114 us at first and 30 and
+// 72 with the rings: twice the instructions for half the products.
 
 constexpr int kAttWarps = 4;
 // Batches in a warp's ring, and CTAs an SM holds. The 64-dim form needs about 180 registers a thread and
@@ -238,7 +246,7 @@ __device__ __forceinline__ int swizzled(int r, int c) {
     return HD == 64 ? c ^ (r >> 1 & 3) : c ^ (r & 7);
 }
 
-// The first `bytes` (2048 or 4096) of a batch's keys and values, and its scales.
+// A batch's keys and values, of which `blocks` blocks are there, and their scales.
 template <int HD>
 __device__ __forceinline__ void fetch_batch(AttnSmem<HD>& sm, int warp, int lane, int stage, const uint8_t* k, const uint8_t* v,
                                             const float* ks, const float* vs, int blocks) {
@@ -581,8 +589,7 @@ __device__ __forceinline__ AttnSmem<HD>& attn_smem() {
     return *reinterpret_cast<AttnSmem<HD>*>(attn_raw);
 }
 
-__device__ __forceinline__ int attn_keys(const AttnArgs& a, int b) {
-    const int pos = a.positions[b];
+__device__ __forceinline__ int attn_keys(const AttnArgs& a, int pos) {
     return pos >= a.max_ctx ? a.max_ctx : max(pos, -1) + 1;
 }
 
@@ -601,8 +608,11 @@ struct SplitPlan {
     int n, each, more;
     __device__ __forceinline__ explicit SplitPlan(const AttnArgs& a) {
         int units = 0;
+        // lane b reads row b's position; from L2, for the joining kernel reads it before it waits
+        const int lane = threadIdx.x & 31;
+        const int own = lane < a.rows ? attn_keys(a, __ldcg(a.positions + lane)) : 0;
 #pragma unroll
-        for (int b = 0; b < kMaxBatch; ++b) keys[b] = b < a.rows ? attn_keys(a, b) : 0;
+        for (int b = 0; b < kMaxBatch; ++b) keys[b] = __shfl_sync(0xffffffffu, own, b);
 #pragma unroll
         for (int b = 0; b < kMaxBatch; ++b) units += attn_share(keys[b]) * a.n_heads;
         constexpr int least = kAttWarps * batch_blocks(HD);   // a batch for each warp
@@ -671,7 +681,7 @@ __global__ void __launch_bounds__(32 * kAttWarps, attn_per_sm(HD)) k_attn_whole(
     AttnSmem<HD>& sm = attn_smem<HD>();
     const int h = blockIdx.x % a.n_heads, b = blockIdx.x / a.n_heads;
     cudaGridDependencySynchronize();     // everything enqueued before has run
-    const int keys = attn_keys(a, b);
+    const int keys = attn_keys(a, a.positions[b]);
     float* out = a.out + ((size_t)b * a.n_heads + h) * a.group * HD;
     if (keys == 0) {
         for (int e = threadIdx.x; e < a.group * HD; e += 32 * kAttWarps) out[e] = 0.f;
@@ -711,8 +721,10 @@ __global__ void __launch_bounds__(32 * kAttWarps, attn_per_sm(HD)) k_attn_split(
     }
 }
 
-// Joins the partials of one (row, query head): warps take slots in turn, lanes the dims.
-constexpr int kJoinWarps = 8, kJoinEach = 4;
+// Joins the partials of one (row, query head): warps take kJoinEach slots in turn, lanes the dims. (8, 8)
+// against (8, 4) warps and slots: 16.1 and 16.8 us for one row of 65536 keys and 8 heads of 64 dims, 9.1 and 11.5
+// with one head (444 partials); 16 warps are no faster there and 1 us slower at 8 x 8 pairs.
+constexpr int kJoinWarps = 8, kJoinEach = 8;
 template <int HD>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_merge_q(const __grid_constant__ AttnArgs a) {
     constexpr int D = HD / 32;

@@ -164,6 +164,31 @@ def test_select_captured_and_replayed():
     assert np.array_equal(tok.cpu().numpy(), t) and np.array_equal(par.cpu().numpy(), p)
 
 
+def test_logits_written_by_the_kernel_just_before():
+    """The selection is placed while the kernel before it ends; what that one wrote has to be seen."""
+    for batch, vocab in ((2, 50257), (40, 4096)):
+        sets = [torch.randn(batch * 4, vocab, device="cuda") for _ in range(3)]
+        scores = torch.zeros(batch, 4, device="cuda")
+        logits = torch.empty_like(sets[0])
+
+        def outs():
+            return [torch.zeros(batch, 8, dtype=torch.int32, device="cuda") for _ in range(2)] + [torch.zeros(batch, 8, device="cuda")]
+
+        want = []
+        for x in sets:
+            o = outs()
+            beam_select(x, scores, *o)
+            torch.cuda.synchronize()
+            want.append(o)
+        got = [outs() for _ in range(150)]
+        for i, o in enumerate(got):
+            logits.fill_(1.0)
+            logits.copy_(sets[i % 3])
+            beam_select(logits, scores, *o)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for i, o in enumerate(got) for a, b in zip(o, want[i % 3]))
+
+
 # ------------------------------------------------------------------ reordering
 
 def test_reorder_captured_and_replayed_with_other_parents():
