@@ -111,6 +111,16 @@ def test_masks_infinities_and_nans(vocab):
     check(x, first, 8)
 
 
+def test_scores_that_are_no_numbers():
+    x, scores, _ = draw(1, 4, 1000, 13)
+    scores[0] = [np.nan, -np.inf, np.inf, -2.0]
+    check(x, scores, 6)
+    scores[0] = [np.nan, np.nan, -np.inf, np.finfo(np.float32).min]
+    check(x, scores, 6)
+    scores[0] = -1e30                                    # so far down that totals of one beam are equal
+    check(x, scores, 6)
+
+
 def test_the_best_logits_all_in_one_place():
     """Everything above the bound sits with a few threads: more is gathered than the list holds."""
     vocab = 128256

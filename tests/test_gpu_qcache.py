@@ -356,6 +356,46 @@ def test_qcache_reorder_against_the_plain_form(layers, rows, heads, dim, max_seq
             assert np.array_equal(got.view(view).cpu().numpy(), reorder(was.view(view).cpu().numpy(), parents, span))
 
 
+def test_a_cache_beyond_32_bit_offsets():
+    """More than 2^32 bytes of codes: the last layer's last planes are stored, attended to and reordered."""
+    g = np.random.default_rng(3)
+    max_seq = 1 << 20
+    c = QCache(shape(3, 6, 128), 2, max_seq)
+    x = [bf16(g, 1, 2, 6, 100, 128).cuda() for _ in range(2)]
+    c.append(x[0], x[1], i32([0, 0]), counts=i32([100, 77]), first_layer=2)
+    c.append(x[0][:, :, :, :64], x[1][:, :, :, :64], i32([max_seq, max_seq - 64]), first_layer=2)  # one does not fit
+    torch.cuda.synchronize()
+    for t, codes, scale in ((x[0], c.k_codes, c.k_scale), (x[1], c.v_codes, c.v_scale)):
+        want, big = quantise(t[0, 1, 5, 32:64].float().cpu().numpy())
+        assert np.array_equal(codes[2, 1, 5, -32:].cpu().numpy(), want) and float(scale[2, 1, 5, -1]) == big
+        assert not codes[2, 0, 5, -64:].any()
+    assert not c.k_codes[:2].any() and not c.v_codes[:2].any()
+    q = torch.from_numpy(g.standard_normal((2, 12, 128)).astype(np.float32)).cuda()
+    check_attention(c, 2, q, [99, 76], max_seq)
+    check_attention(c, 2, q, [99, 76], 128)
+    k0, v0, t0 = c.k_codes[2, 0].clone(), c.v_codes[2, 1].clone(), c.k_tail[2].clone()
+    c.reorder(i32([1, 0]), i32([100, 77]))
+    torch.cuda.synchronize()
+    assert torch.equal(c.k_codes[2, 1, :, :96], k0[:, :96]) and torch.equal(c.v_codes[2, 0, :, :64], v0[:, :64])
+    assert torch.equal(c.k_tail[2, 0, :, :13], t0[1, :, :13]) and torch.equal(c.k_tail[2, 1, :, :4], t0[0, :, :4])
+
+
+def test_tensors_on_the_host_are_refused():
+    c = QCache(shape(1, 1, 64), 1, 64)
+    x, q = torch.zeros(1, 1, 1, 2, 64, dtype=torch.bfloat16), torch.zeros(1, 4, 64)
+    with pytest.raises(AssertionError):
+        c.append(x, x, i32([0]))
+    with pytest.raises(AssertionError):
+        c.attention(0, q, i32([0]), q.cuda())
+    with pytest.raises(AssertionError):
+        c.attention(0, q.cuda(), torch.zeros(1, dtype=torch.int32), q.cuda())
+    with pytest.raises(AssertionError):
+        c.attention(0, q.cuda(), torch.zeros(1, dtype=torch.int64, device="cuda"), q.cuda())
+    with pytest.raises(AssertionError):
+        c.reorder(i32([0]), torch.zeros(1, dtype=torch.int32))
+    assert not c.k_tail.any()
+
+
 # ------------------------------------------------------------------ decode steps on it
 
 @pytest.mark.parametrize("batch, past", [(1, 5), (3, 28), (2, 130)])
