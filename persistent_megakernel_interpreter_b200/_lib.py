@@ -2,7 +2,8 @@
 
 Argument marshalling only: every step of the decode path runs in the library's
 CUDA kernels. Loading fails loudly when the library is missing; there is no
-fallback.
+fallback. The calls between steps (beam selection, reordering, the 8-bit cache) go
+through the compiled part of the binding, ``call()``.
 """
 from __future__ import annotations
 
@@ -138,6 +139,23 @@ def lib() -> ctypes.CDLL:
         getattr(L, f).restype = st
     _lib = L
     return L
+
+
+_call = None
+
+
+def call():
+    """The compiled binding of the calls between decode steps (raises if it was not built)."""
+    global _call
+    if _call is None:
+        lib()
+        if not os.path.exists(os.path.join(_HERE, "_call.so")):
+            raise RuntimeError(f"{_HERE}/_call.so is missing; build it with "
+                               "`python -m persistent_megakernel_interpreter_b200.build`")
+        import torch  # noqa: F401  (it links to torch's libraries)
+        from . import _call as module
+        _call = module
+    return _call
 
 
 def check(code: int, what: str) -> None:

@@ -1,13 +1,16 @@
-"""Build libmk.so in-tree with nvcc for sm_100a (no JIT, no torch extension).
+"""Build libmk.so in-tree with nvcc for sm_100a (no JIT, no torch in it), and _call.so,
+the compiled part of the Python binding, with g++ against torch's headers.
 
 ``python -m persistent_megakernel_interpreter_b200.build`` or ``build_library()``.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +21,8 @@ LIB = os.path.join(PKG, "libmk.so")
 SOURCES = ["api.cu", "megakernel.cu", "megakernel_trace.cu", "baseline.cu", "noalloc.cu", "select.cu", "beam.cu",
            "reorder.cu", "qcache.cu", "pack.cpp", "schedule.cpp"]
 HEADERS = ["mk_internal.h", "mk_device.cuh", "pack.h", "qcache.h"]
+CALL = os.path.join(PKG, "_call.so")
+CALL_SOURCE = os.path.join(CSRC, "binding.cpp")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -26,6 +31,32 @@ def _nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found")
+
+
+def _call_stale() -> bool:
+    if not os.path.exists(CALL):
+        return True
+    t = os.path.getmtime(CALL)
+    return any(os.path.getmtime(d) > t for d in (CALL_SOURCE, os.path.join(INCLUDE, "mk.h"), os.path.abspath(__file__)))
+
+
+def _build_call(verbose: bool) -> None:
+    """Compile the binding against torch's headers; it links to libmk.so beside it."""
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    tmp = f"{CALL}.tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-I{INCLUDE}",
+           f"-I{os.path.join(torch, 'include')}", f"-I{os.path.join(torch, 'include', 'torch', 'csrc', 'api', 'include')}",
+           f"-I{sysconfig.get_paths()['include']}", f"-I{cuda}", CALL_SOURCE, "-o", tmp, f"-L{PKG}", "-l:libmk.so",
+           "-Wl,-rpath,$ORIGIN", f"-L{os.path.join(torch, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    try:
+        subprocess.check_call(cmd)
+        os.replace(tmp, CALL)
+    finally:
+        if os.path.exists(tmp):
+            os.remove(tmp)
 
 
 def _stale() -> bool:
@@ -38,8 +69,10 @@ def _stale() -> bool:
 
 
 def build_library(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    """Compile every source to an object in parallel, then link libmk.so."""
+    """Compile every source to an object in parallel, then link libmk.so; then the binding."""
     if not force and not _stale():
+        if _call_stale():
+            _build_call(verbose)
         return LIB
     tag = f".tmp{os.getpid()}"
     common = [_nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -63,6 +96,8 @@ def build_library(force: bool = False, verbose: bool = False, extra: list[str] |
         for o in objs:
             if os.path.exists(o):
                 os.remove(o)
+    if force or _call_stale():
+        _build_call(verbose)
     return LIB
 
 

@@ -12,7 +12,6 @@ PyTorch supplies device memory and streams only.
 from __future__ import annotations
 
 import ctypes
-import functools
 
 import torch
 
@@ -38,12 +37,7 @@ def _at(t: torch.Tensor, dtype: torch.dtype, n: int, device: int) -> int:
 
 
 def _raw_stream(stream, device: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
-
-
-# The current device of a thread that already holds CUDA tensors (torch.cuda.current_device without its
-# initialisation check, which costs as much as a launch).
-_current_device = torch._C._cuda_getDevice
+    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
 
 
 class Megakernel:
@@ -144,7 +138,7 @@ class Megakernel:
         """One step as ordinary kernels on an 8-bit cache (``qcache.QCache``); it needs no schedule, and
         contexts may be as long as the cache. ``status`` (int32 [1], optional) receives the step's
         device status. Without a ``workspace`` one is allocated for the call."""
-        device = _current_device()
+        device = torch.cuda.current_device()
         batch = tokens.numel()
         max_ctx = min(cache.max_seq, self.max_seq) if max_ctx is None else max_ctx
         if workspace is None:
@@ -259,28 +253,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, next_tokens: torch.T
     ``eos`` at its own score; ``next_finished`` receives who is finished then. ``positions``
     (optional, one per row) are advanced by one. ``next_scores`` may be ``scores`` and
     ``next_finished`` may be ``finished``."""
-    device = _current_device()
-    rows, vocab = logits.shape
-    batch, beams = scores.shape
-    out_batch, n_out = next_tokens.shape
-    n_in, n = batch * beams, batch * n_out
-    assert rows == n_in and out_batch == batch and logits.get_device() == device and logits.dtype is torch.float32
-    stride, inner = logits.stride()
-    assert inner == 1 or vocab == 1
-    _lib.check(_lib.lib().mk_beam_select(
-        logits.data_ptr(), stride if rows > 1 else vocab, batch, beams, vocab, n_out,
-        _at(scores, torch.float32, n_in, device), None if finished is None else _at(finished, torch.int32, n_in, device),
-        eos, _at(next_tokens, torch.int32, n, device), _at(parents, torch.int32, n, device),
-        _at(next_scores, torch.float32, n, device),
-        None if next_finished is None else _at(next_finished, torch.int32, n, device),
-        None if positions is None else _at(positions, torch.int32, n_in, device), _raw_stream(stream, device)),
-        "mk_beam_select")
-
-
-@functools.lru_cache(maxsize=64)
-def _cache_shape(n_layers: int, max_batch: int, heads: int, max_seq: int, dim: int):
-    """The part of a config that says how a cache is laid out, as an argument."""
-    return ctypes.byref(_lib.MkConfig(n_layers, 0, 0, heads, dim, 0, 0, 0.0, 0.0, max_batch, max_seq))
+    _lib.check(_lib.call().beam_select(logits, scores, next_tokens, parents, next_scores, finished, eos, next_finished,
+                                       positions, stream), "mk_beam_select")
 
 
 def cache_reorder(k_cache: torch.Tensor, v_cache: torch.Tensor, parents: torch.Tensor, lengths: torch.Tensor,
@@ -289,15 +263,7 @@ def cache_reorder(k_cache: torch.Tensor, v_cache: torch.Tensor, parents: torch.T
     starts[r] .. lengths[parents[r]] - 1, all rows at once and in place, asynchronous on ``stream``: beams
     that follow ``beam_select``, a sequence forked into free rows, live rows moved over finished ones.
     A parent that is the row itself or no row (-1) leaves the row as it is."""
-    device = _current_device()
-    rows = parents.numel()
-    n_layers, max_batch, heads, max_seq, dim = k_cache.shape
-    assert v_cache.shape == k_cache.shape
-    _lib.check(_lib.lib().mk_cache_reorder(
-        _cache_shape(n_layers, max_batch, heads, max_seq, dim), _at(k_cache, torch.bfloat16, 1, device), _at(v_cache, torch.bfloat16, 1, device), rows,
-        _at(parents, torch.int32, rows, device), _at(lengths, torch.int32, rows, device),
-        None if starts is None else _at(starts, torch.int32, rows, device), _raw_stream(stream, device)),
-        "mk_cache_reorder")
+    _lib.check(_lib.call().cache_reorder(k_cache, v_cache, parents, lengths, starts, stream), "mk_cache_reorder")
 
 
 def plan_schedule(cfg: ModelConfig, batch: int, max_ctx: int, n_sm: int, max_batch: int = 8,

@@ -15,10 +15,8 @@ import torch
 
 from . import _lib
 from .config import ModelConfig
-from .model import _at, _current_device, _raw_stream
 
 BLOCK = _lib.QCACHE_BLOCK
-_Strides = ctypes.c_int64 * 4
 
 
 class QCache:
@@ -59,37 +57,19 @@ class QCache:
         self._c = _lib.MkQcache(n_layers, max_batch, n_heads, max_seq, dim, 0, k_codes.data_ptr(),
                                 v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k_tail.data_ptr(),
                                 v_tail.data_ptr())
-        self._ref = ctypes.byref(self._c)
+        self._ref, self._address = ctypes.byref(self._c), ctypes.addressof(self._c)
 
     def append(self, k, v, positions, counts=None, first_layer: int = 0, stream=None) -> None:
         """Stores ``k`` and ``v`` (bf16 [layers][rows][heads][tokens][dim], any strides with the dims
         contiguous) from slot ``positions[row]`` on: ``counts[row]`` tokens of each row (all of them
         where ``counts`` is None), in layers ``first_layer`` on."""
-        device = _current_device()
-        layers, rows, heads, tokens, dim = shape = k.shape
-        strides = k.stride()
-        assert v.shape == shape and heads == self.n_kv_heads and dim == self.head_dim and strides[4] == 1
-        assert k.dtype is torch.bfloat16 and v.dtype is torch.bfloat16
-        assert k.get_device() == device and v.get_device() == device and self._device == device
-        if v.stride() != strides or (strides[0] | strides[1] | strides[2] | strides[3]) & 7:
-            # the stride of a dimension of one is any number
-            strides = [s if n > 1 else 0 for s, n in zip(strides, shape)]
-            assert strides == [s if n > 1 else 0 for s, n in zip(v.stride(), shape)]
-        _lib.check(_lib.lib().mk_qcache_append(
-            self._ref, first_layer, layers, rows, tokens, k.data_ptr(), v.data_ptr(), _Strides(strides[0], strides[1], strides[2], strides[3]),
-            _at(positions, torch.int32, rows, device),
-            None if counts is None else _at(counts, torch.int32, rows, device), _raw_stream(stream, device)),
-            "mk_qcache_append")
+        _lib.check(_lib.call().qcache_append(self._address, self._device, k, v, positions, counts, first_layer, stream),
+                   "mk_qcache_append")
 
     def reorder(self, parents, lengths, starts=None, stream=None) -> None:
         """Row r takes over row parents[r]'s slots starts[r] .. lengths[parents[r]] - 1, all rows at once."""
-        device = _current_device()
-        rows = parents.numel()
-        assert self._device == device
-        _lib.check(_lib.lib().mk_qcache_reorder(
-            self._ref, rows, _at(parents, torch.int32, rows, device), _at(lengths, torch.int32, rows, device),
-            None if starts is None else _at(starts, torch.int32, rows, device), _raw_stream(stream, device)),
-            "mk_qcache_reorder")
+        _lib.check(_lib.call().qcache_reorder(self._address, self._device, parents, lengths, starts, stream),
+                   "mk_qcache_reorder")
 
     def attention_workspace(self, rows: int, n_heads: int, max_ctx: int):
         """A workspace for ``attention`` calls of this size, or None where they need none. Calls that
@@ -101,21 +81,13 @@ class QCache:
         """out[row][head] = attention of q[row][head] (fp32 [rows][n_heads][dim]) over slots
         0 .. positions[row] of ``layer``; a negative position gives zeros. ``max_ctx``: no row has more
         slots (max_seq where None). Without a ``workspace`` one is allocated for the call."""
-        device = _current_device()
-        rows, n_heads, dim = q.shape
-        n = rows * n_heads * dim
-        assert dim == self.head_dim and self._device == device
         max_ctx = self.max_seq if max_ctx is None else max_ctx
         if workspace is None:
+            rows, n_heads = q.shape[:2]
             if stream is None:
                 workspace = self.attention_workspace(rows, n_heads, max_ctx)
             else:
                 with torch.cuda.stream(stream):  # its memory is given back in the order of that stream
                     workspace = self.attention_workspace(rows, n_heads, max_ctx)
-        at, size = None, 0
-        if workspace is not None:
-            at, size = _at(workspace, torch.uint8, 1, device), workspace.numel()
-        _lib.check(_lib.lib().mk_qcache_attention(
-            self._ref, layer, rows, n_heads, max_ctx, _at(q, torch.float32, n, device),
-            _at(positions, torch.int32, rows, device), _at(out, torch.float32, n, device), at, size,
-            _raw_stream(stream, device)), "mk_qcache_attention")
+        _lib.check(_lib.call().qcache_attention(self._address, self._device, layer, q, positions, out, max_ctx, workspace,
+                                                stream), "mk_qcache_attention")

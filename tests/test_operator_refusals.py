@@ -132,3 +132,33 @@ def test_cache_struct_matches_the_c_header(tmp_path):
                            str(tmp_path / "q")])
     got = [int(x) for x in subprocess.run([str(tmp_path / "q")], capture_output=True, text=True, check=True).stdout.split()]
     assert got == [ctypes.sizeof(_lib.MkQcache), _lib.QCACHE_BLOCK] + [getattr(_lib.MkQcache, f).offset for f in fields]
+
+
+def test_compiled_binding_refuses_before_it_calls():
+    """Host tensors, wrong kinds of arguments and wrong counts of them raise; no CUDA device is asked for."""
+    import torch
+    call = _lib.call()
+    x, s, t = torch.zeros(2, 8), torch.zeros(1, 2), torch.zeros(1, 2, dtype=torch.int32)
+    with pytest.raises(AssertionError, match="logits"):
+        call.beam_select(x, s, t, t, s, None, -1, None, None, None)
+    with pytest.raises(AssertionError, match="logits: a tensor"):
+        call.beam_select(None, s, t, t, s, None, -1, None, None, None)
+    with pytest.raises(TypeError):
+        call.beam_select(x, s)
+    with pytest.raises(AssertionError, match="k_cache"):
+        call.cache_reorder(x, x, t, t, None, None)
+    c = _lib.MkQcache(1, 1, 1, 64, 64, 0, *([4096] * 6))
+    at = ctypes.addressof(c)
+    with pytest.raises(AssertionError, match="k: "):
+        call.qcache_append(at, 0, x, x, t, None, 0, None)
+    with pytest.raises(AssertionError, match="parents"):
+        call.qcache_reorder(at, 0, t, t, None, None)
+    with pytest.raises(AssertionError, match="q: "):
+        call.qcache_attention(at, 0, 0, x, t, x, 64, None, None)
+
+
+def test_missing_binding_fails_loudly(monkeypatch, tmp_path):
+    monkeypatch.setattr(_lib, "_call", None)
+    monkeypatch.setattr(_lib, "_HERE", str(tmp_path))
+    with pytest.raises(RuntimeError, match="missing"):
+        _lib.call()
