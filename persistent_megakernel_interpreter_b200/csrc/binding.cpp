@@ -4,7 +4,7 @@
 // be moved, and checking eight tensors in Python and passing them through ctypes takes
 // as long again (measured: 7.0 us a call against 3.5).
 //
-// Each function returns the library's mk_status; a tensor of the wrong type, device or
+// Each call returns the library's mk_status; a tensor of the wrong type, device or
 // size raises AssertionError before the library is called.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -234,12 +234,23 @@ PyObject* qcache_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// cache, rows, n_heads, max_ctx: the bytes of workspace an attention call needs
+PyObject* qcache_attention_workspace(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 4, [&] {
+        const void* c = PyLong_AsVoidPtr(a[0]);
+        if (!c && PyErr_Occurred()) throw Refused{};
+        return mk_qcache_attention_workspace(static_cast<const mk_qcache*>(c), (int)number(a[1], "rows"), (int)number(a[2], "n_heads"),
+                                             (int)number(a[3], "max_ctx"));
+    });
+}
+
 PyMethodDef methods[] = {
     {"beam_select", (PyCFunction)(void*)beam_select, METH_FASTCALL, nullptr},
     {"cache_reorder", (PyCFunction)(void*)cache_reorder, METH_FASTCALL, nullptr},
     {"qcache_append", (PyCFunction)(void*)qcache_append, METH_FASTCALL, nullptr},
     {"qcache_reorder", (PyCFunction)(void*)qcache_reorder, METH_FASTCALL, nullptr},
     {"qcache_attention", (PyCFunction)(void*)qcache_attention, METH_FASTCALL, nullptr},
+    {"qcache_attention_workspace", (PyCFunction)(void*)qcache_attention_workspace, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_call", "Checked calls into libmk.so.", -1, methods, nullptr, nullptr, nullptr, nullptr};

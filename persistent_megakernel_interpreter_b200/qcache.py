@@ -74,7 +74,7 @@ class QCache:
     def attention_workspace(self, rows: int, n_heads: int, max_ctx: int):
         """A workspace for ``attention`` calls of this size, or None where they need none. Calls that
         may overlap on the GPU need one each."""
-        n = _lib.lib().mk_qcache_attention_workspace(self._ref, rows, n_heads, max_ctx)
+        n = _lib.call().qcache_attention_workspace(self._address, rows, n_heads, max_ctx)
         return torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
 
     def attention(self, layer: int, q, positions, out, max_ctx: int | None = None, workspace=None, stream=None) -> None:
