@@ -483,22 +483,33 @@ __device__ __forceinline__ void attn_blocks(const AttnArgs& a, AttnSmem<HD>& sm,
 }
 
 // The open block's n < 32 bf16 tokens, fp32 on the CUDA cores: warp h takes head h,
-// lane i scores token i, then each lane sums HD / 32 dims.
+// lane i scores token i, then each lane sums HD / 32 dims. At 64 dims its loads go out with the first
+// batches', ahead of the wait for the queries (129 keys 3.8 -> 3.5 us); at 128 that many more registers
+// spill (53.7 -> 55.2 us at 4 x 60001 keys). Half the values' follow behind the scores.
 template <int HD>
-__device__ __forceinline__ void attn_tail(const AttnArgs& a, AttnSmem<HD>& sm, size_t plane, int n, int warp, int lane) {
-    if (warp >= a.group) return;
-    const uint16_t* kt = a.tail[0] + plane * (kQBlock * HD) + (size_t)min(lane, n - 1) * HD;
-    const uint16_t* vt = a.tail[1] + plane * (kQBlock * HD) + lane * (HD / 32);
-    // every load is issued before the first is used, half the values' behind the scores
-    constexpr int D = HD / 32, H = kQBlock / 2;
+struct AttnTail {
+    static constexpr int D = HD / 32, H = kQBlock / 2;
     uint4 kr[HD / 8];
     uint32_t vr[H][D / 2];
+    const uint16_t* vt;
+    __device__ __forceinline__ void load_values(int first, int n) {
 #pragma unroll
-    for (int e = 0; e < HD / 8; ++e) kr[e] = *reinterpret_cast<const uint4*>(kt + 8 * e);
+        for (int i = 0; i < H; ++i)
 #pragma unroll
-    for (int i = 0; i < H; ++i)
+            for (int d = 0; d < D / 2; ++d) vr[i][d] = *reinterpret_cast<const uint32_t*>(vt + min(first + i, n - 1) * HD + 2 * d);
+    }
+    __device__ __forceinline__ void load(const AttnArgs& a, size_t plane, int n, int lane) {
+        const uint16_t* kt = a.tail[0] + plane * (kQBlock * HD) + (size_t)min(lane, n - 1) * HD;
+        vt = a.tail[1] + plane * (kQBlock * HD) + lane * D;
 #pragma unroll
-        for (int d = 0; d < D / 2; ++d) vr[i][d] = *reinterpret_cast<const uint32_t*>(vt + min(i, n - 1) * HD + 2 * d);
+        for (int e = 0; e < HD / 8; ++e) kr[e] = *reinterpret_cast<const uint4*>(kt + 8 * e);
+        load_values(0, n);
+    }
+    __device__ __forceinline__ void attend(AttnSmem<HD>& sm, int n, int warp, int lane);
+};
+
+template <int HD>
+__device__ __forceinline__ void AttnTail<HD>::attend(AttnSmem<HD>& sm, int n, int warp, int lane) {
     float s = 0.f;
 #pragma unroll
     for (int e = 0; e < HD / 8; ++e)
@@ -523,12 +534,7 @@ __device__ __forceinline__ void attn_tail(const AttnArgs& a, AttnSmem<HD>& sm, s
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         if (half * H >= n) break;
-        if (half == 1) {
-#pragma unroll
-            for (int i = 0; i < H; ++i)
-#pragma unroll
-                for (int d = 0; d < D / 2; ++d) vr[i][d] = *reinterpret_cast<const uint32_t*>(vt + min(H + i, n - 1) * HD + 2 * d);
-        }
+        if (half == 1) load_values(H, n);
         // tokens behind the last (the last one's values) weigh nothing
 #pragma unroll
         for (int i = 0; i < H; ++i) {
@@ -660,14 +666,19 @@ __device__ __forceinline__ uint32_t attn_range(const AttnArgs& a, AttnSmem<HD>& 
         qv[i] = e < a.group * HD ? q[e] : 0.f;
     }
     src.start(sm, warp, lane);
+    // the open block, by the warps of the group's heads
+    const int nt = stop > nb && warp < a.group ? keys - nb * kQBlock : 0;
+    AttnTail<HD> tail;
+    if (HD == 64 && nt) tail.load(a, plane, nt, lane);
 #pragma unroll
     for (int i = 0; i < QE; ++i) (&sm.q[0][0])[i * 32 * kAttWarps + threadIdx.x] = qv[i];
     __syncthreads();
     uint32_t parts = 0;
-    if (stop > nb) {
-        attn_tail<HD>(a, sm, plane, keys - nb * kQBlock, warp, lane);
-        parts = 1u << kAttWarps;
+    if (nt) {
+        if (HD != 64) tail.load(a, plane, nt, lane);
+        tail.attend(sm, nt, warp, lane);
     }
+    if (stop > nb) parts = 1u << kAttWarps;
     if (src.b0 < src.b1) {
         attn_blocks<HD>(a, sm, src, warp, lane);
         parts |= (1u << kAttWarps) - 1;
