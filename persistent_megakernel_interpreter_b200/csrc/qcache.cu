@@ -229,13 +229,20 @@ struct AttnSmem {
     float tail_o[kMaxGroupHeads][HD];
     float m[kAttWarps + 1][kMaxGroupHeads];
     float l[kAttWarps + 1][kMaxGroupHeads];
-    float q[kMaxGroupHeads][HD];
-    // Part p's output of head h: a warp's lies in its own ring once the ring is drained.
-    __device__ __forceinline__ float* o(int p, int h) {
-        return p == kAttWarps ? tail_o[h] : reinterpret_cast<float*>(ring[p]) + h * HD;
+    // The queries, in quarters of a head (what one lane of a fragment reads) 16 bytes apart, so that the
+    // lanes' 16-byte reads meet every bank once.
+    static constexpr int kQuarter = HD / 4 + 4;
+    alignas(16) float q[kMaxGroupHeads][4][kQuarter];
+    __device__ __forceinline__ float& query(int h, int d) { return q[h][d / (HD / 4)][d % (HD / 4)]; }
+    // Part p's output of head h, dim d: a warp's lie in its own ring once the ring is drained, an eighth of a
+    // head (what one lane writes) and the heads 16 bytes apart, for the same reason.
+    static constexpr int kEighth = HD / 8 + 4, kHead = 8 * kEighth + 4;
+    __device__ __forceinline__ float* warp_o(int p, int h) { return reinterpret_cast<float*>(ring[p]) + h * kHead; }
+    __device__ __forceinline__ float o(int p, int h, int d) {
+        return p == kAttWarps ? tail_o[h][d] : warp_o(p, h)[d / (HD / 8) * kEighth + d % (HD / 8)];
     }
 };
-static_assert(kMaxGroupHeads * 128 * sizeof(float) <= 2 * kHalf, "a warp's outputs lie in its ring");
+static_assert(kMaxGroupHeads * AttnSmem<128>::kHead * sizeof(float) <= 2 * kHalf, "a warp's outputs lie in its ring");
 
 // The 16-byte piece c of row r sits at piece swizzled(r, c) of its row, so that the
 // fragment reads below meet every bank once: of eight lanes that read a piece of keys in
@@ -309,9 +316,13 @@ __device__ __forceinline__ void attn_blocks(const AttnArgs& a, AttnSmem<HD>& sm,
     float kmul;
     const uint32_t sel_q = up ? 0x5140u : 0x7362u;   // (lower, lower, upper, upper) digits of two elements
     {
-        float big = 0.f;
+        float big = 0.f, q[HD / 4];
         bool bad = false;
-        const float* q = sm.q[head < a.group ? head : 0] + t * (HD / 4);
+#pragma unroll
+        for (int e = 0; e < HD / 4; e += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(&sm.q[head < a.group ? head : 0][t][e]);
+            q[e] = v.x; q[e + 1] = v.y; q[e + 2] = v.z; q[e + 3] = v.w;
+        }
 #pragma unroll
         for (int e = 0; e < HD / 4; ++e) {
             big = fmaxf(big, fabsf(q[e]));
@@ -474,11 +485,13 @@ __device__ __forceinline__ void attn_blocks(const AttnArgs& a, AttnSmem<HD>& sm,
         sm.l[warp][g] = l;
     }
 #pragma unroll
-    for (int i = 0; i < VD; ++i)
+    for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float x = o[i][e] + __shfl_xor_sync(0xffffffffu, o[i][e], 16);
-            if (g < a.group) sm.o(warp, g)[(2 * t + e) * VD + i] = x;
+        for (int i = 0; i < VD; i += 4) {
+            float4 x;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) (&x.x)[k] = o[i + k][e] + __shfl_xor_sync(0xffffffffu, o[i + k][e], 16);
+            if (g < a.group) *reinterpret_cast<float4*>(sm.warp_o(warp, g) + (2 * t + e) * sm.kEighth + i) = x;
         }
 }
 
@@ -516,8 +529,8 @@ __device__ __forceinline__ void AttnTail<HD>::attend(AttnSmem<HD>& sm, int n, in
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t w = (&kr[e].x)[i];
-            s = fmaf(__uint_as_float(w << 16), sm.q[warp][8 * e + 2 * i], s);
-            s = fmaf(__uint_as_float(w & 0xffff0000u), sm.q[warp][8 * e + 2 * i + 1], s);
+            s = fmaf(__uint_as_float(w << 16), sm.query(warp, 8 * e + 2 * i), s);
+            s = fmaf(__uint_as_float(w & 0xffff0000u), sm.query(warp, 8 * e + 2 * i + 1), s);
         }
     s = lane < n ? s * (kLog2e * (HD == 64 ? 0.125f : 0.08838834764831845f)) : -INFINITY;
     float m = s;
@@ -569,7 +582,7 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, AttnSmem<HD>& sm, u
             const bool there = parts >> p & 1;
             m[p] = there ? sm.m[p][h] : -INFINITY;
             ls[p] = there ? sm.l[p][h] : 0.f;
-            x[p] = there ? sm.o(p, h)[d] : 0.f;
+            x[p] = there ? sm.o(p, h, d) : 0.f;
             M = fmaxf(M, m[p]);
         }
         float l = 0.f, y = 0.f;
@@ -671,7 +684,10 @@ __device__ __forceinline__ uint32_t attn_range(const AttnArgs& a, AttnSmem<HD>& 
     AttnTail<HD> tail;
     if (HD == 64 && nt) tail.load(a, plane, nt, lane);
 #pragma unroll
-    for (int i = 0; i < QE; ++i) (&sm.q[0][0])[i * 32 * kAttWarps + threadIdx.x] = qv[i];
+    for (int i = 0; i < QE; ++i) {
+        const int e = i * 32 * kAttWarps + (int)threadIdx.x;
+        sm.query(e / HD, e % HD) = qv[i];
+    }
     __syncthreads();
     uint32_t parts = 0;
     if (nt) {
