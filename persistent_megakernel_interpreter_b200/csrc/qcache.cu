@@ -155,9 +155,9 @@ __global__ void __launch_bounds__(32 * kAppWarps, 8) k_append(const __grid_const
 // join at the end.
 //
 // Bound by HBM: 2 * dim bytes a key and KV head. Measured on one B200: 4 rows of up to 60001 keys of 128 dims
-// (308 MB) in 53.4 us, 5.76 TB/s (88% of the measured copy rate); 8 rows of up to 16384 keys of 64 dims (105 MB)
-// in 22.1 us (73%); 129 keys in 3.8 us. Around the stream of bytes there are about 6 us: 1.5 to launch, 0.7
-// for the plan, 1.5 until the first batch is here, 1 to join a CTA's warps, 2 for the joining kernel. As fp16
+// (308 MB) in 51.5 us, 5.97 TB/s (91% of the measured copy rate); 8 rows of up to 16384 keys of 64 dims (105 MB)
+// in 21.6 us (75%); 129 keys in 3.2 us. Around the stream of bytes there are about 5 us: 1.5 to launch, 0.7
+// for the plan, 1 until the first batch is here, 0.7 to join a CTA's warps, 1.5 for the joining kernel. As fp16
 // products (codes converted, the other operand in two parts) the same took 32 and 114 us at first and 30 and
 // 72 with the rings: twice the instructions for half the products.
 
@@ -614,8 +614,8 @@ __device__ __forceinline__ int attn_keys(const AttnArgs& a, int pos) {
 
 // The order in which the split deals out blocks: row by row, head by head, each (row, KV head) with its
 // blocks (the open one included) behind kPad units without work, which stand for what starting and
-// joining one more piece costs the CTA that has them. 0 / 8 / 16 / 24 / 32 units: 61.1 / 58.8 / 57.0 /
-// 56.4 / 56.4 us at 4 x 60001 keys of 128 dims.
+// joining one more piece costs the CTA that has them. 4 / 8 / 12 / 16 / 24 units: 52.4 / 52.3 / 51.6 /
+// 51.7 / 51.7 us at 4 x 60001 keys of 128 dims, 22.0 / 21.7 / 21.9 / 21.6 / 21.5 at 8 x 16384 of 64.
 constexpr int kPad = 24;
 __device__ __forceinline__ int attn_units(int keys) { return (keys + kQBlock - 1) / kQBlock; }
 __device__ __forceinline__ int attn_share(int keys) { return keys ? attn_units(keys) + kPad : 0; }
@@ -834,10 +834,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_merge_q(const __grid_c
 // ------------------------------------------------------------------ launches
 
 // One CTA per (row, KV head) up to these contexts, in one kernel; beyond, the split and its joining kernel.
-// With 8 pairs the two take 5.1 and 5.3 us at 1024 keys of 64 dims, 7.6 and 5.4 at 2048; 6.9 and 7.7 at 512 keys of
-// 128, 9.4 and 7.7 at 1024. With 64 pairs 7.8 and 9.5 us at 2048 keys of 64 dims, 13.0 and 11.4 at 4096;
-// 14.7 and 17.2 at 2048 of 128, 28 and 21 at 4096.
-bool attn_is_split(int hd, int pairs, int max_ctx) { return max_ctx > (pairs >= 32 ? 2048 : 65536 / hd); }
+// With 8 pairs the two take 4.8 and 4.7 us at 1024 keys of 64 dims, 7.5 and 4.9 at 2048; 5.4 and 5.7 at 512 keys of
+// 128, 8.1 and 5.8 at 1024. With 64 pairs 7.6 and 8.0 us at 2048 keys of 64 dims, 12.9 and 9.7 at 4096;
+// 8.2 and 9.2 at 1024 of 128, 13.5 and 10.8 at 2048.
+bool attn_is_split(int hd, int pairs, int max_ctx) { return max_ctx > (pairs >= 32 ? 131072 : 65536) / hd; }
 // Floats of the partials' maxima and sums; the outputs behind them are read 16 bytes at a time.
 size_t attn_ml_floats(size_t slots) { return (2 * slots + 3) / 4 * 4; }
 int attn_ctas(int hd) { return kQSms * attn_per_sm(hd); }

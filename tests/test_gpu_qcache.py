@@ -210,7 +210,7 @@ def test_attention_over_long_contexts(dim, heads, rows, n):
 @pytest.mark.parametrize("rows, heads, group", [(1, 1, 1), (3, 1, 3), (1, 5, 1), (5, 7, 2)])
 def test_attention_on_either_side_of_its_two_forms(dim, rows, heads, group):
     """Contexts at the border between one CTA per pair and the split, and one past it; odd numbers of partials."""
-    for max_ctx in (65536 // dim, 65536 // dim + 1, 2048, 2049):
+    for max_ctx in (65536 // dim, 65536 // dim + 1, 131072 // dim, 131072 // dim + 1):
         lengths = [max(0, max_ctx - 31 * r - r * r) for r in range(rows)]
         c, g = filled(1, rows, heads, dim, max_ctx, lengths, max_ctx + rows)
         q = torch.from_numpy(g.standard_normal((rows, heads * group, dim)).astype(np.float32)).cuda()
