@@ -144,8 +144,13 @@ __global__ void __launch_bounds__(32 * kAppWarps, 8) k_append(const __grid_const
 // h + 12, so lanes of groups g < 4 and g >= 4 hold two digits each of head g % 4.
 //   scores:  q as 30-bit whole numbers (its head's largest magnitude sets the step)
 //   outputs: weights as 32-bit whole numbers, 2^31 m 2^(s + e - M), where 2^e m is the
-//            block's value scale (1 <= m < 2) and M the running maximum of s + e; the
-//            softmax's sum is that of 2^(s + e - M) 2^-e.
+//            block's value scale (1 <= m < 2) and M the running maximum of s + e, rounded up
+// The softmax's sum l is that of 2^(s - M + 39): of the scores alone, for the weight of a block whose values
+// are far smaller than another's rounds to nothing while its keys still count. With -67 <= e <= 121 (blocks
+// below 2^-60 are zeros, and a block of zeros counts as e = -67, so that it never sets the size that
+// others' weights are held relative to) a term is at most 2^106, 2^20 of them stay finite, and one that is flushed
+// to zero is below 2^-44 of the largest. M is a whole number, so every change of unit is by an exact
+// power of two; one exponential serves a key's weight and its term of the sum.
 // Accumulators start at the bits of 1.5 * 2^23, so that read as a float they are that
 // plus the sum (below 2^22 in magnitude: 128 * 127 * 128 in a score, 255 * 127 * 64 in
 // an output), and one FMA turns each into its share of the fp32 result.
@@ -170,8 +175,6 @@ __host__ __device__ constexpr int attn_per_sm(int hd) { return hd == 64 ? 2 : 3;
 constexpr int kHalf = 4096;            // bytes of a batch's keys, and of its values
 __host__ __device__ constexpr int batch_blocks(int hd) { return hd == 64 ? 2 : 1; }
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr uint32_t kMagicBits = 0x4b400000u;
-constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
 
 struct AttnArgs {
     const uint8_t* codes[2];
@@ -204,6 +207,18 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+constexpr int kLeastScale = -67;       // of a value block: 2^-60 / 127 = 1.008 * 2^-67
+constexpr int kSumBits = 39;           // sums are in units of 2^(M - 39)
+constexpr float kSumUnit = 0x1p39f;
+// Powers of two for whole numbers d <= 0, from d's place in the bits of kMagic + d: 2^d itself (no less than 2^-126)
+// and l 2^d for a sum l (positive, or a NaN that stays one), to which d may do more than one number holds.
+constexpr uint32_t kMagicBits = 0x4b400000u;
+constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
+__device__ __forceinline__ float pow2(float d) { return __uint_as_float(__float_as_uint(fmaxf(d, -126.0f) + (kMagic + 127.0f)) << 23); }
+__device__ __forceinline__ float scaled(float l, float d) {
+    const int by = (int)(__float_as_uint(fmaxf(d, -252.0f) + kMagic) << 23);
+    return fmaf(l, 0.0f, __int_as_float(max(__float_as_int(l) + by, 0)));
+}
 
 // C += A B, C read and written as 32-bit whole numbers; A's bytes signed (queries) or not (weights).
 __device__ __forceinline__ void mma_s8(uint32_t (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -226,7 +241,7 @@ struct AttnSmem {
     static constexpr int kStages = attn_stages(HD);
     alignas(16) uint8_t ring[kAttWarps][kStages][2][kHalf];
     float scale[kAttWarps][kStages][2][2];   // keys' and values', of the batch's blocks
-    float tail_o[kMaxGroupHeads][HD];
+    alignas(16) float tail_o[kMaxGroupHeads][HD];
     float m[kAttWarps + 1][kMaxGroupHeads];
     float l[kAttWarps + 1][kMaxGroupHeads];
     // The queries, in quarters of a head (what one lane of a fragment reads) 16 bytes apart, so that the
@@ -362,7 +377,6 @@ __device__ __forceinline__ void attn_blocks(const AttnArgs& a, AttnSmem<HD>& sm,
     const bool odd = HD == 64 && (t & 1);
     const uint32_t sel_lo = odd ? 0x1504u : 0x5140u, sel_hi = odd ? 0x3726u : 0x7362u;
     float M = -1e30f, l = 0.f, o[VD][2];
-    int e_ref = 0;
 #pragma unroll
     for (int i = 0; i < VD; ++i) o[i][0] = o[i][1] = 0.f;
     const int b1 = src.b1;
@@ -373,24 +387,20 @@ __device__ __forceinline__ void attn_blocks(const AttnArgs& a, AttnSmem<HD>& sm,
         src.fetch(sm, warp, lane, blk + (kStages - 1) * src.kStep, stage == 0 ? kStages - 1 : stage - 1);
         const uint8_t* kp = sm.ring[warp][stage][0];
         const uint8_t* vp = sm.ring[warp][stage][1];
-        float ks[BB], ef[BB], vm[BB], inv[BB];
+        float ks[BB];
+        uint32_t vs[BB];                     // the bits of 2^e m
+        int ev[BB];
 #pragma unroll
         for (int b = 0; b < BB; ++b) {
             ks[b] = sm.scale[warp][stage][0][b] * kmul;
-            const uint32_t vs = __float_as_uint(sm.scale[warp][stage][1][b]);
-            // 2^e m; a block of zeros (scale 0) adds nothing to O, and any e serves its share of the sum
-            int e = vs == 0u ? e_ref : (int)(vs >> 23) - 127;
-            const bool nan = e > 127;
-            e = nan ? 0 : e;
-            if (b == 0 || blk + b < b1) e_ref = e;
-            ef[b] = (float)e;
-            vm[b] = __uint_as_float((vs & 0x7fffffu) | (127u + 31u) << 23);
-            inv[b] = nan ? __uint_as_float(0x7fffffffu) : __uint_as_float((uint32_t)(127 - e) << 23);
-            if (b > 0 && blk + b >= b1) inv[b] = 0.f;
+            vs[b] = __float_as_uint(sm.scale[warp][stage][1][b]);
+            ev[b] = max((int)(vs[b] >> 23) - 127, kLeastScale);
         }
         stage = stage == kStages - 1 ? 0 : stage + 1;
         // lane (g, t) ends with the score of head g % 4 and key 8 n + 2 t, + 1 for g >= 4
-        float s[NT], top = -INFINITY;
+        float s[NT], most[BB];               // most: the lane's largest score of a block, rounded up
+#pragma unroll
+        for (int b = 0; b < BB; ++b) most[b] = -INFINITY;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             uint32_t acc[4] = {kMagicBits, kMagicBits, kMagicBits, kMagicBits};
@@ -404,27 +414,40 @@ __device__ __forceinline__ void attn_blocks(const AttnArgs& a, AttnSmem<HD>& sm,
             s[n] = (up ? f1 : f0) + __shfl_xor_sync(0xffffffffu, up ? f0 : f1, 16);
             const int b = n / (kQBlock / 8);
             if (b > 0 && blk + b >= b1) s[n] = -INFINITY;
-            else top = fmaxf(top, fmaf(s[n], ks[b], ef[b]));
+            else most[b] = fmaxf(most[b], s[n] * ks[b]);
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < BB; ++b) {
+            most[b] = fmaxf(ceilf(most[b]), -1e30f);
+            if (b == 0 || blk + b < b1) top = fmaxf(top, most[b] + (float)ev[b]);
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-        const float Mn = fmaxf(M, top), f = ex2(M - Mn);
+        const float Mn = fmaxf(M, top);
+        const float f = pow2(M - Mn);
+        l = scaled(l, M - Mn);
         M = Mn;
-        l *= f;
         uint32_t wp[NT];                     // the pair's digits
 #pragma unroll
         for (int b = 0; b < BB; ++b) {
-            const float off = ef[b] - M;
+            const bool none = b > 0 && blk + b >= b1;
+            // what the lane's exponentials, 2^(s - most), still lack: as a weight 2^31 m 2^(most + e - M), as a term
+            // of the sum 2^(most - M + 39)
+            const int k = __float_as_int(fmaxf(most[b] + (float)ev[b] - M, -400.0f) + kMagic) - (int)kMagicBits;
+            const float vm = __uint_as_float((vs[b] & 0x7fffffu) | (uint32_t)max(k + 127 + 31, 0) << 23);
+            const float unit = __uint_as_float((uint32_t)max(k - ev[b] + 127 + kSumBits, 0) << 23);
             float sum = 0.f;
 #pragma unroll
             for (int n = b * (kQBlock / 8); n < (b + 1) * (kQBlock / 8); ++n) {
-                const float w = b > 0 && blk + b >= b1 ? 0.f : ex2(fmaf(s[n], ks[b], off));
+                const float w = none ? 0.f : ex2(fmaf(s[n], ks[b], -most[b]));
                 sum += w;
-                const uint32_t W = __float2uint_rn(w * vm[b]);
+                const uint32_t W = __float2uint_rn(w * vm);
                 wp[n] = __byte_perm(W, __shfl_xor_sync(0xffffffffu, W, 16), sel_w);
             }
-            l = fmaf(sum, inv[b], l);
+            // a NaN scale's bits are those of a NaN
+            l = fmaf(sum, vs[b] > 0x7f800000u && !none ? __uint_as_float(0x7fffffffu) : unit, l);
         }
         uint32_t pa[NT / 4][4];
 #pragma unroll
@@ -536,7 +559,7 @@ __device__ __forceinline__ void AttnTail<HD>::attend(AttnSmem<HD>& sm, int n, in
     float m = s;
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-    m = fmaxf(m, -1e30f);
+    m = fmaxf(ceilf(m), -1e30f);             // e = 0
     const float w = lane < n ? exp2f(s - m) : 0.f;
     float l = w;
 #pragma unroll
@@ -561,41 +584,69 @@ __device__ __forceinline__ void AttnTail<HD>::attend(AttnSmem<HD>& sm, int n, in
     }
     if (lane == 0) {
         sm.m[kAttWarps][warp] = m;
-        sm.l[kAttWarps][warp] = l;
+        sm.l[kAttWarps][warp] = l * kSumUnit;
     }
 #pragma unroll
     for (int d = 0; d < D; ++d) sm.tail_o[warp][lane * D + d] = o[d];
 }
 
-// Joins the parts in sm whose mask bit is set. FINAL: the output row; else a partial.
+// Two or four consecutive floats. The loads stay in their order, ahead of the shuffles that follow.
+__device__ __forceinline__ void load(const float* p, float (&x)[2]) {
+    asm volatile("ld.global.v2.f32 {%0, %1}, [%2];" : "=f"(x[0]), "=f"(x[1]) : "l"(p));
+}
+__device__ __forceinline__ void load(const float* p, float (&x)[4]) {
+    asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "l"(p));
+}
+__device__ __forceinline__ void store(float* p, const float (&x)[2]) { *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]); }
+__device__ __forceinline__ void store(float* p, const float (&x)[4]) { *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]); }
+
+// The largest and the sum of eight lanes.
+__device__ __forceinline__ float max_of_8(float x) {
+#pragma unroll
+    for (int k = 4; k > 0; k >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
+    return x;
+}
+__device__ __forceinline__ float sum_of_8(float x) {
+#pragma unroll
+    for (int k = 4; k > 0; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
+    return x;
+}
+
+// Joins the parts in sm whose mask bit is set. FINAL: the output row; else a partial. Warp h has head h, so
+// that a thread forms each part's factor once.
 template <int HD, bool FINAL>
 __device__ __forceinline__ void attn_join(const AttnArgs& a, AttnSmem<HD>& sm, uint32_t parts, float* o, float* ml) {
     __syncthreads();
-    constexpr int QE = kMaxGroupHeads * HD / (32 * kAttWarps);
-#pragma unroll
-    for (int i = 0; i < QE; ++i) {
-        const int e = i * 32 * kAttWarps + (int)threadIdx.x, h = e / HD, d = e % HD;
-        if (h >= a.group) break;
-        float m[kAttWarps + 1], x[kAttWarps + 1], ls[kAttWarps + 1], M = -INFINITY;
+    static_assert(kMaxGroupHeads <= kAttWarps, "a warp for every head");
+    constexpr int D = HD / 32;
+    const int h = threadIdx.x >> 5, d = (threadIdx.x & 31) * D;
+    if (h < a.group) {
+        float m[kAttWarps + 1], x[kAttWarps + 1][D], ls[kAttWarps + 1], M = -INFINITY;
 #pragma unroll
         for (int p = 0; p <= kAttWarps; ++p) {
             const bool there = parts >> p & 1;
             m[p] = there ? sm.m[p][h] : -INFINITY;
             ls[p] = there ? sm.l[p][h] : 0.f;
-            x[p] = there ? sm.o(p, h, d) : 0.f;
+#pragma unroll
+            for (int i = 0; i < D; ++i) x[p][i] = there ? sm.o(p, h, d + i) : 0.f;
             M = fmaxf(M, m[p]);
         }
-        float l = 0.f, y = 0.f;
+        float l = 0.f, y[D];
+#pragma unroll
+        for (int i = 0; i < D; ++i) y[i] = 0.f;
 #pragma unroll
         for (int p = 0; p <= kAttWarps; ++p) {
-            const float f = ex2(m[p] - M);
-            l = fmaf(f, ls[p], l);
-            y = fmaf(f, x[p], y);
+            const float w = pow2(m[p] - M);
+            l += scaled(ls[p], m[p] - M);
+#pragma unroll
+            for (int i = 0; i < D; ++i) y[i] = fmaf(w, x[p][i], y[i]);
         }
         if (FINAL) {
-            o[e] = y / l;
+            l *= 1.0f / kSumUnit;
+#pragma unroll
+            for (int i = 0; i < D; ++i) o[h * HD + d + i] = y[i] / l;
         } else {
-            o[e] = y;
+            store(o + h * HD + d, y);
             if (d == 0) *reinterpret_cast<float2*>(ml + 2 * h) = make_float2(M, l);
         }
     }
@@ -770,40 +821,59 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_merge_q(const __grid_c
     first += h * share;
     const int c0 = share ? P.owner(first + kPad) : 0, total = share ? P.owner(first + share - 1) - c0 + 1 : 0;
     cudaGridDependencySynchronize();
-    // kJoinEach partials of a warp at once, every load issued before the first is used
+    // kJoinEach partials of a warp at once, every load issued before the first is used. At 128 dims lane k of every
+    // eight forms the factor of the k-th partial and shuffles pass it (2 rows of 4096 keys and 8 heads: 8.8 us, 9.0 where every
+    // lane forms all eight), at 64 dims every lane forms them (6.1 us, 6.3 with shuffles).
     float M = -INFINITY, l = 0.f, o[D];
 #pragma unroll
     for (int d = 0; d < D; ++d) o[d] = 0.f;
+    const size_t slot = (size_t)c0 + pair;
     for (int i = warp * kJoinEach; i < total; i += kJoinWarps * kJoinEach) {
-        float2 ml[kJoinEach];
         float p[kJoinEach][D];
+        auto at = [&](int k) { return (slot + min(i + k, total - 1)) * a.group + hg; };
+        if constexpr (D == 4) {
+            static_assert(kJoinEach == 8, "a lane for each");
+            float ml[2];
+            load(a.part_ml + at(lane & 7) * 2, ml);
 #pragma unroll
-        for (int k = 0; k < kJoinEach; ++k) {
-            const size_t at = ((size_t)c0 + min(i + k, total - 1) + pair) * a.group + hg;
-            ml[k] = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
-            if constexpr (D == 2) {
-                const float2 x = *reinterpret_cast<const float2*>(a.part_o + at * HD + lane * D);
-                p[k][0] = x.x; p[k][1] = x.y;
-            } else {
-                const float4 x = *reinterpret_cast<const float4*>(a.part_o + at * HD + lane * D);
-                p[k][0] = x.x; p[k][1] = x.y; p[k][2] = x.z; p[k][3] = x.w;
+            for (int k = 0; k < kJoinEach; ++k) load(a.part_o + at(k) * HD + lane * D, p[k]);
+            const bool there = i + (lane & 7) < total;
+            const float Mn = fmaxf(M, max_of_8(ml[0])), f = pow2(M - Mn), own = there ? pow2(ml[0] - Mn) : 0.f;
+            l = scaled(l, M - Mn) + sum_of_8(there ? scaled(ml[1], ml[0] - Mn) : 0.f);
+            M = Mn;
+#pragma unroll
+            for (int d = 0; d < D; ++d) o[d] *= f;
+#pragma unroll
+            for (int k = 0; k < kJoinEach; ++k) {
+                const float w = __shfl_sync(0xffffffffu, own, k);
+#pragma unroll
+                for (int d = 0; d < D; ++d) o[d] = fmaf(p[k][d], w, o[d]);
             }
-            if (i + k >= total) ml[k] = make_float2(-INFINITY, 0.f);   // a partial's maximum is never below -1e30
-        }
-        float Mn = M;
+        } else {
+            float2 ml[kJoinEach];
 #pragma unroll
-        for (int k = 0; k < kJoinEach; ++k) Mn = fmaxf(Mn, ml[k].x);
-        const float f = exp2f(M - Mn);
-        M = Mn;
-        l *= f;
+            for (int k = 0; k < kJoinEach; ++k) {
+                ml[k] = *reinterpret_cast<const float2*>(a.part_ml + at(k) * 2);
+                const float2 x = *reinterpret_cast<const float2*>(a.part_o + at(k) * HD + lane * D);
+                p[k][0] = x.x;
+                p[k][1] = x.y;
+                if (i + k >= total) ml[k] = make_float2(-INFINITY, 0.f);   // a partial's maximum is never below -1e30
+            }
+            float Mn = M;
 #pragma unroll
-        for (int d = 0; d < D; ++d) o[d] *= f;
+            for (int k = 0; k < kJoinEach; ++k) Mn = fmaxf(Mn, ml[k].x);
+            const float f = pow2(M - Mn);
+            l = scaled(l, M - Mn);
+            M = Mn;
 #pragma unroll
-        for (int k = 0; k < kJoinEach; ++k) {
-            const float w = exp2f(ml[k].x - M);
-            l = fmaf(ml[k].y, w, l);
+            for (int d = 0; d < D; ++d) o[d] *= f;
 #pragma unroll
-            for (int d = 0; d < D; ++d) o[d] = fmaf(p[k][d], w, o[d]);
+            for (int k = 0; k < kJoinEach; ++k) {
+                const float w = pow2(ml[k].x - M);
+                l += scaled(ml[k].y, ml[k].x - M);
+#pragma unroll
+                for (int d = 0; d < D; ++d) o[d] = fmaf(p[k][d], w, o[d]);
+            }
         }
     }
 #pragma unroll
@@ -824,11 +894,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_merge_q(const __grid_c
     float top = -INFINITY, L = 0.f, x = 0.f;
     for (int i = 0; i < used; ++i) top = fmaxf(top, sm[i]);
     for (int i = 0; i < used; ++i) {
-        const float f = exp2f(sm[i] - top);
-        L = fmaf(f, sl[i], L);
-        x = fmaf(f, so[i][e], x);
+        L += scaled(sl[i], sm[i] - top);
+        x = fmaf(pow2(sm[i] - top), so[i][e], x);
     }
-    out[e] = x / L;
+    out[e] = x / (L * (1.0f / kSumUnit));
 }
 
 // ------------------------------------------------------------------ launches
