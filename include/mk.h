@@ -354,9 +354,12 @@ mk_status mk_qcache_reorder(const mk_qcache* c, int rows, const int32_t* parents
 /* Decode attention of one layer over the 8-bit cache, one query token per row: for each row r and query
  * head h, out = sum_s softmax_s(q . k_s / sqrt(head_dim)) v_s over the slots s = 0 .. positions[r] of
  * KV head h / (n_heads / n_kv_heads).
+ *   positions     device int32 [rows]: the row's last token, or another one of its open block; it says which
+ *                 of the row's blocks are closed and so held as codes. For an earlier slot of a row that holds more,
+ *                 call mk_qcache_attention_prefix, unless it is the last slot of a closed block
  *   n_heads       a multiple of n_kv_heads, at most 4 query heads per KV head (else MK_ERR_UNSUPPORTED)
- *   max_ctx       positions[r] + 1 <= max_ctx <= max_seq; a larger position reads the first max_ctx
- *                 slots, a negative one (an empty row) gives zeros
+ *   max_ctx       1..max_seq: at most the first max_ctx slots of a row are read (a larger position is still
+ *                 where the row ends); a negative position (an empty row) gives zeros
  *   q, out        device fp32 [rows][n_heads][head_dim]
  *   workspace     device, 16-byte aligned, mk_qcache_attention_workspace() bytes; need not be
  *                 initialised, belongs to the call until it has run (calls that overlap on the GPU
@@ -370,7 +373,13 @@ mk_status mk_qcache_attention(const mk_qcache* c, int layer, int rows, int n_hea
                               const int32_t* positions, float* out, void* workspace, size_t workspace_bytes,
                               void* stream);
 
-/* Bytes of workspace a mk_qcache_attention call with these arguments needs (0 also for arguments it
+/* The same for any slots of a row: attends to s = 0 .. positions[r] of a row that holds lengths[r] tokens (device
+ * int32 [rows]; positions and max_ctx beyond it stop at it). */
+mk_status mk_qcache_attention_prefix(const mk_qcache* c, int layer, int rows, int n_heads, int max_ctx, const float* q,
+                                     const int32_t* positions, const int32_t* lengths, float* out, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace either attention call with these arguments needs (0 also for arguments it
  * refuses). */
 size_t mk_qcache_attention_workspace(const mk_qcache* c, int rows, int n_heads, int max_ctx);
 

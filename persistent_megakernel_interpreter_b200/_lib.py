@@ -125,6 +125,7 @@ def lib() -> ctypes.CDLL:
     L.mk_qcache_append.argtypes = [qc, i, i, i, i, P, P, ctypes.POINTER(ctypes.c_int64), P, P, P]
     L.mk_qcache_reorder.argtypes = [qc, i, P, P, P, P]
     L.mk_qcache_attention.argtypes = [qc, i, i, i, i, P, P, P, P, ctypes.c_size_t, P]
+    L.mk_qcache_attention_prefix.argtypes = [qc, i, i, i, i, P, P, P, P, P, ctypes.c_size_t, P]
     L.mk_qcache_attention_workspace.argtypes = [qc, i, i, i]
     L.mk_qcache_attention_workspace.restype = ctypes.c_size_t
     L.mk_decode_step_qcache.argtypes = [P, qc, i, i, P, P, P, P, ctypes.c_size_t, P, P]
@@ -135,7 +136,7 @@ def lib() -> ctypes.CDLL:
               "mk_get_schedule_info", "mk_read_counters", "mk_pack_weights_host", "mk_read_trace",
               "mk_baseline_decode_step_noalloc", "mk_greedy_select", "mk_tensor_map_specs_host",
               "mk_beam_select", "mk_cache_reorder", "mk_qcache_append", "mk_qcache_reorder", "mk_qcache_attention",
-              "mk_decode_step_qcache"):
+              "mk_qcache_attention_prefix", "mk_decode_step_qcache"):
         getattr(L, f).restype = st
     _lib = L
     return L

@@ -214,9 +214,9 @@ PyObject* qcache_reorder(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// cache, its device, layer, q, positions, out, max_ctx, workspace, stream
+// cache, its device, layer, q, positions, out, max_ctx, workspace, stream[, lengths]
 PyObject* qcache_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 9, [&] {
+    return guarded(n, n == 10 ? 10 : 9, [&] {
         const at::Tensor& q = tensor(a[3], "q");
         const int device = device_of(q, "q");
         const mk_qcache* c = qcache_of(a[0], a[1], device);
@@ -230,7 +230,12 @@ PyObject* qcache_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         void* work = at_least_or_null<void>(a[7], "workspace", kU8, 1, device);
         const size_t size = work ? (size_t)THPVariable_Unpack(a[7]).numel() : 0;
         void* stream = stream_of(a[8], device);
-        return unlocked([&] { return mk_qcache_attention(c, layer, (int)rows, (int)heads, max_ctx, qp, pos, out, work, size, stream); });
+        const int32_t* len = n == 10 ? at_least_or_null<int32_t>(a[9], "lengths", kI32, rows, device) : nullptr;
+        return unlocked([&] {
+            if (len)
+                return mk_qcache_attention_prefix(c, layer, (int)rows, (int)heads, max_ctx, qp, pos, len, out, work, size, stream);
+            return mk_qcache_attention(c, layer, (int)rows, (int)heads, max_ctx, qp, pos, out, work, size, stream);
+        });
     });
 }
 

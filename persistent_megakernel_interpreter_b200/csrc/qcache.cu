@@ -183,6 +183,7 @@ struct AttnArgs {
     int layer, max_batch, n_heads, group, max_seq, n_blocks, rows, max_ctx;
     const float* q;               // [rows][n_heads * group][HD]
     const int32_t* positions;
+    const int32_t* lengths;       // tokens that each row holds; NULL: positions[row] + 1
     float* out;
     float* part_ml;               // [slots][group][2]
     float* part_o;                // [slots][group][HD]
@@ -287,14 +288,15 @@ __device__ __forceinline__ void fetch_batch(AttnSmem<HD>& sm, int warp, int lane
     if (lane < 2 * blocks) copy4(&sm.scale[warp][stage][lane & 1][lane >> 1], (lane & 1 ? vs : ks) + (lane >> 1));
 }
 
-// The closed blocks [b0, b1) of one (row, KV head): where they lie, and a warp's fetches of them. Warp w
-// takes the batches at b0 + (w + 4 i) batch_blocks.
+// The closed blocks [b0, b1) of one (row, KV head), of whose slots those below `keys` are attended to: where they
+// lie, and a warp's fetches of them. Warp w takes the batches at b0 + (w + 4 i) batch_blocks.
 template <int HD>
 struct AttnSource {
     const uint8_t *k, *v;
     const float *ks, *vs;
-    int b0, b1;
-    __device__ __forceinline__ AttnSource(const AttnArgs& a, size_t plane, int first, int last) : b0(first), b1(last) {
+    int b0, b1, keys;
+    __device__ __forceinline__ AttnSource(const AttnArgs& a, size_t plane, int first, int last, int n)
+        : b0(first), b1(last), keys(min(n, last * kQBlock)) {
         k = a.codes[0] + plane * a.max_seq * HD;
         v = a.codes[1] + plane * a.max_seq * HD;
         ks = a.scale[0] + plane * a.n_blocks;
@@ -389,10 +391,14 @@ __device__ __forceinline__ void attn_blocks(const AttnArgs& a, AttnSmem<HD>& sm,
         const uint8_t* vp = sm.ring[warp][stage][1];
         float ks[BB];
         uint32_t vs[BB];                     // the bits of 2^e m
-        int ev[BB];
+        int ev[BB], left[BB];
 #pragma unroll
         for (int b = 0; b < BB; ++b) {
-            ks[b] = sm.scale[warp][stage][0][b] * kmul;
+            // the block's keys that count, from the lane's first on (of the 32 that are its own and its pair's)
+            left[b] = src.keys - (blk + b) * kQBlock - 2 * t - up;
+            // never zero: what a key behind the last gets, -infinity, has to stay that
+            ks[b] = b == 0 || blk + b < b1 ? sm.scale[warp][stage][0][b] * kmul : 1.0f;
+            ks[b] = ks[b] == 0.f ? 1e-38f : ks[b];
             vs[b] = __float_as_uint(sm.scale[warp][stage][1][b]);
             ev[b] = max((int)(vs[b] >> 23) - 127, kLeastScale);
         }
@@ -413,14 +419,14 @@ __device__ __forceinline__ void attn_blocks(const AttnArgs& a, AttnSmem<HD>& sm,
             const float f0 = sum_of(acc[0], sm0) + sum_of(acc[2], sm1), f1 = sum_of(acc[1], sm0) + sum_of(acc[3], sm1);
             s[n] = (up ? f1 : f0) + __shfl_xor_sync(0xffffffffu, up ? f0 : f1, 16);
             const int b = n / (kQBlock / 8);
-            if (b > 0 && blk + b >= b1) s[n] = -INFINITY;
-            else most[b] = fmaxf(most[b], s[n] * ks[b]);
+            if (8 * (n % (kQBlock / 8)) >= left[b]) s[n] = -INFINITY;
+            most[b] = fmaxf(most[b], s[n] * ks[b]);
         }
         float top = -INFINITY;
 #pragma unroll
         for (int b = 0; b < BB; ++b) {
             most[b] = fmaxf(ceilf(most[b]), -1e30f);
-            if (b == 0 || blk + b < b1) top = fmaxf(top, most[b] + (float)ev[b]);
+            top = fmaxf(top, most[b] + (float)ev[b]);
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -432,7 +438,6 @@ __device__ __forceinline__ void attn_blocks(const AttnArgs& a, AttnSmem<HD>& sm,
         uint32_t wp[NT];                     // the pair's digits
 #pragma unroll
         for (int b = 0; b < BB; ++b) {
-            const bool none = b > 0 && blk + b >= b1;
             // what the lane's exponentials, 2^(s - most), still lack: as a weight 2^31 m 2^(most + e - M), as a term
             // of the sum 2^(most - M + 39)
             const int k = __float_as_int(fmaxf(most[b] + (float)ev[b] - M, -400.0f) + kMagic) - (int)kMagicBits;
@@ -441,13 +446,13 @@ __device__ __forceinline__ void attn_blocks(const AttnArgs& a, AttnSmem<HD>& sm,
             float sum = 0.f;
 #pragma unroll
             for (int n = b * (kQBlock / 8); n < (b + 1) * (kQBlock / 8); ++n) {
-                const float w = none ? 0.f : ex2(fmaf(s[n], ks[b], -most[b]));
+                const float w = ex2(fmaf(s[n], ks[b], -most[b]));
                 sum += w;
                 const uint32_t W = __float2uint_rn(w * vm);
                 wp[n] = __byte_perm(W, __shfl_xor_sync(0xffffffffu, W, 16), sel_w);
             }
             // a NaN scale's bits are those of a NaN
-            l = fmaf(sum, vs[b] > 0x7f800000u && !none ? __uint_as_float(0x7fffffffu) : unit, l);
+            l = fmaf(sum, vs[b] > 0x7f800000u && (b == 0 || blk + b < b1) ? __uint_as_float(0x7fffffffu) : unit, l);
         }
         uint32_t pa[NT / 4][4];
 #pragma unroll
@@ -659,9 +664,19 @@ __device__ __forceinline__ AttnSmem<HD>& attn_smem() {
     return *reinterpret_cast<AttnSmem<HD>*>(attn_raw);
 }
 
-__device__ __forceinline__ int attn_keys(const AttnArgs& a, int pos) {
-    return pos >= a.max_ctx ? a.max_ctx : max(pos, -1) + 1;
-}
+// The slots that row b attends to, and whether the last of them lie in its open block. A row's length says which of
+// its blocks are closed: a cut inside a closed block is read from the codes.
+struct RowKeys {
+    int n;
+    bool open;
+    __device__ __forceinline__ RowKeys(const AttnArgs& a, int b) {
+        // from L2, for the joining kernel reads them before it waits
+        const int pos = __ldcg(a.positions + b), length = a.lengths ? min(__ldcg(a.lengths + b), a.max_seq) : min(pos, a.max_seq - 1) + 1;
+        n = max(min(min(pos, a.max_ctx - 1) + 1, length), 0);
+        open = n > length / kQBlock * kQBlock;
+    }
+    __device__ __forceinline__ RowKeys(int keys, bool in_open) : n(keys), open(in_open) {}
+};
 
 // The order in which the split deals out blocks: row by row, head by head, each (row, KV head) with its
 // blocks (the open one included) behind kPad units without work, which stand for what starting and
@@ -675,14 +690,16 @@ __device__ __forceinline__ int attn_share(int keys) { return keys ? attn_units(k
 template <int HD>
 struct SplitPlan {
     int keys[kMaxBatch];                 // of each row
+    uint32_t open;                       // the rows whose open block is attended to
     int n, each, more;
     __device__ __forceinline__ explicit SplitPlan(const AttnArgs& a) {
         int units = 0;
-        // lane b reads row b's position; from L2, for the joining kernel reads it before it waits
+        // lane b reads row b's
         const int lane = threadIdx.x & 31;
-        const int own = lane < a.rows ? attn_keys(a, __ldcg(a.positions + lane)) : 0;
+        const RowKeys own = lane < a.rows ? RowKeys(a, lane) : RowKeys(0, false);
 #pragma unroll
-        for (int b = 0; b < kMaxBatch; ++b) keys[b] = __shfl_sync(0xffffffffu, own, b);
+        for (int b = 0; b < kMaxBatch; ++b) keys[b] = __shfl_sync(0xffffffffu, own.n, b);
+        open = __ballot_sync(0xffffffffu, own.open);
 #pragma unroll
         for (int b = 0; b < kMaxBatch; ++b) units += attn_share(keys[b]) * a.n_heads;
         constexpr int least = kAttWarps * batch_blocks(HD);   // a batch for each warp
@@ -712,14 +729,14 @@ struct SplitPlan {
     }
 };
 
-// Blocks [u, stop) of one (row, KV head) with `keys` keys, the open one included, into the
+// Blocks [u, stop) of one (row, KV head) that attends to `keys`, the open one included, into the
 // parts of sm: which, as bits.
 template <int HD>
-__device__ __forceinline__ uint32_t attn_range(const AttnArgs& a, AttnSmem<HD>& sm, int b, int h, int u, int stop, int keys) {
+__device__ __forceinline__ uint32_t attn_range(const AttnArgs& a, AttnSmem<HD>& sm, int b, int h, int u, int stop, RowKeys keys) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const size_t plane = ((size_t)a.layer * a.max_batch + b) * a.n_heads + h;
-    const int nb = keys / kQBlock;
-    const AttnSource<HD> src(a, plane, u, min(stop, nb));
+    const int nb = keys.open ? keys.n / kQBlock : attn_units(keys.n);
+    const AttnSource<HD> src(a, plane, u, min(stop, nb), keys.n);
     // the queries' loads go out ahead of the many of the first batches
     constexpr int QE = kMaxGroupHeads * HD / (32 * kAttWarps);
     const float* q = a.q + ((size_t)b * a.n_heads + h) * a.group * HD;
@@ -731,7 +748,7 @@ __device__ __forceinline__ uint32_t attn_range(const AttnArgs& a, AttnSmem<HD>& 
     }
     src.start(sm, warp, lane);
     // the open block, by the warps of the group's heads
-    const int nt = stop > nb && warp < a.group ? keys - nb * kQBlock : 0;
+    const int nt = stop > nb && warp < a.group ? keys.n - nb * kQBlock : 0;
     AttnTail<HD> tail;
     if (HD == 64 && nt) tail.load(a, plane, nt, lane);
 #pragma unroll
@@ -759,13 +776,13 @@ __global__ void __launch_bounds__(32 * kAttWarps, attn_per_sm(HD)) k_attn_whole(
     AttnSmem<HD>& sm = attn_smem<HD>();
     const int h = blockIdx.x % a.n_heads, b = blockIdx.x / a.n_heads;
     cudaGridDependencySynchronize();     // everything enqueued before has run
-    const int keys = attn_keys(a, a.positions[b]);
+    const RowKeys keys(a, b);
     float* out = a.out + ((size_t)b * a.n_heads + h) * a.group * HD;
-    if (keys == 0) {
+    if (keys.n == 0) {
         for (int e = threadIdx.x; e < a.group * HD; e += 32 * kAttWarps) out[e] = 0.f;
         return;
     }
-    const uint32_t parts = attn_range<HD>(a, sm, b, h, 0, attn_units(keys), keys);
+    const uint32_t parts = attn_range<HD>(a, sm, b, h, 0, attn_units(keys.n), keys);
     attn_join<HD, true>(a, sm, parts, out, nullptr);
 }
 
@@ -791,7 +808,7 @@ __global__ void __launch_bounds__(32 * kAttWarps, attn_per_sm(HD)) k_attn_split(
         // without the padding; a piece of nothing but padding is no piece
         const int from = max(u - base - kPad, 0), stop = end - base - kPad;
         if (stop > from) {
-            const uint32_t parts = attn_range<HD>(a, sm, b, h, from, stop, keys);
+            const uint32_t parts = attn_range<HD>(a, sm, b, h, from, stop, RowKeys(keys, P.open >> b & 1));
             const size_t slot = (size_t)c + b * a.n_heads + h;
             attn_join<HD, false>(a, sm, parts, a.part_o + slot * a.group * HD, a.part_ml + slot * a.group * 2);
         }
@@ -986,9 +1003,11 @@ extern "C" size_t mk_qcache_attention_workspace(const mk_qcache* c, int rows, in
     return (mk::attn_ml_floats(slots) + slots * (size_t)c->head_dim) * sizeof(float);
 }
 
-extern "C" mk_status mk_qcache_attention(const mk_qcache* c, int layer, int rows, int n_heads, int max_ctx,
-                                         const float* q, const int32_t* positions, float* out, void* workspace,
-                                         size_t workspace_bytes, void* stream) {
+namespace mk {
+// lengths: NULL for rows that hold positions[r] + 1 tokens.
+static mk_status attention(const mk_qcache* c, int layer, int rows, int n_heads, int max_ctx, const float* q,
+                           const int32_t* positions, const int32_t* lengths, float* out, void* workspace,
+                           size_t workspace_bytes, void* stream) {
     if (!q || !positions || !out) return MK_ERR_INVALID_ARG;
     if (const mk_status st = mk::qcache_check(c); st != MK_OK) return st;
     if (n_heads < c->n_kv_heads || n_heads % c->n_kv_heads != 0 || n_heads / c->n_kv_heads > mk::kMaxGroupHeads)
@@ -1015,6 +1034,7 @@ extern "C" mk_status mk_qcache_attention(const mk_qcache* c, int layer, int rows
     a.max_ctx = max_ctx;
     a.q = q;
     a.positions = positions;
+    a.lengths = lengths;
     a.out = out;
     if (need) {
         a.n_cta = mk::attn_ctas(c->head_dim);
@@ -1024,4 +1044,18 @@ extern "C" mk_status mk_qcache_attention(const mk_qcache* c, int layer, int rows
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = c->head_dim == 64 ? mk::attn_launch<64>(a, st) : mk::attn_launch<128>(a, st);
     return e == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+}
+}  // namespace mk
+
+extern "C" mk_status mk_qcache_attention(const mk_qcache* c, int layer, int rows, int n_heads, int max_ctx,
+                                         const float* q, const int32_t* positions, float* out, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+    return mk::attention(c, layer, rows, n_heads, max_ctx, q, positions, nullptr, out, workspace, workspace_bytes, stream);
+}
+
+extern "C" mk_status mk_qcache_attention_prefix(const mk_qcache* c, int layer, int rows, int n_heads, int max_ctx,
+                                                const float* q, const int32_t* positions, const int32_t* lengths,
+                                                float* out, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!lengths) return MK_ERR_INVALID_ARG;
+    return mk::attention(c, layer, rows, n_heads, max_ctx, q, positions, lengths, out, workspace, workspace_bytes, stream);
 }

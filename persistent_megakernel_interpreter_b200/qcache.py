@@ -77,10 +77,13 @@ class QCache:
         n = _lib.call().qcache_attention_workspace(self._address, rows, n_heads, max_ctx)
         return torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
 
-    def attention(self, layer: int, q, positions, out, max_ctx: int | None = None, workspace=None, stream=None) -> None:
+    def attention(self, layer: int, q, positions, out, max_ctx: int | None = None, workspace=None, stream=None,
+                  lengths=None) -> None:
         """out[row][head] = attention of q[row][head] (fp32 [rows][n_heads][dim]) over slots
-        0 .. positions[row] of ``layer``; a negative position gives zeros. ``max_ctx``: no row has more
-        slots (max_seq where None). Without a ``workspace`` one is allocated for the call."""
+        0 .. positions[row] of ``layer``; a negative position gives zeros. ``max_ctx``: at most the first
+        max_ctx slots of a row are read (max_seq where None). ``lengths`` (int32 [rows]): the tokens that
+        each row holds. Where it is None a position has to be the row's last token, another one of its
+        open block, or the last of a closed block. Without a ``workspace`` one is allocated for the call."""
         max_ctx = self.max_seq if max_ctx is None else max_ctx
         if workspace is None:
             rows, n_heads = q.shape[:2]
@@ -90,4 +93,4 @@ class QCache:
                 with torch.cuda.stream(stream):  # its memory is given back in the order of that stream
                     workspace = self.attention_workspace(rows, n_heads, max_ctx)
         _lib.check(_lib.call().qcache_attention(self._address, self._device, layer, q, positions, out, max_ctx, workspace,
-                                                stream), "mk_qcache_attention")
+                                                stream, lengths), "mk_qcache_attention")

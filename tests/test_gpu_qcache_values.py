@@ -98,3 +98,76 @@ def test_values_of_sizes_far_apart(dim, n, first, second):
     q = normal(g, 1, 4, dim)
     q[0, 0] = 0
     rows.check(q, [n - 1], n, extra=2.0 ** -22 * 100)
+
+
+# ------------------------------------------------------------------ slots before a row's last
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads, group", [(2, 4), (3, 1)])
+@pytest.mark.parametrize("lengths, cuts", [([1000, 992, 40, 650], [650, 641, 672, 1, 33, 991]),
+                                           ([2500, 2496, 2490, 1100], [2489, 1999, 1025, 2496, 70])])
+def test_max_ctx_cuts_rows_anywhere(dim, heads, group, lengths, cuts):
+    """max_ctx inside closed blocks, inside the open one and at their borders, with rows that end before it."""
+    g = np.random.default_rng(dim + heads)
+    rows, slots = len(lengths), max(lengths)
+    k, v = (normal(g, rows, heads, slots, dim).bfloat16() for _ in range(2))
+    rows_ = Rows(k, v, lengths)
+    for cut in cuts:
+        q = normal(g, rows, heads * group, dim)
+        rows_.check(q, [n - 1 for n in lengths], cut, keys=[min(n, cut) for n in lengths])
+        rows_.check(q, [n - 1 for n in lengths], cut, keys=[min(n, cut) for n in lengths], lengths=i32(lengths))
+
+
+def test_positions_far_beyond_max_ctx():
+    """The largest position means a full cache, whose last block is open where max_seq is no multiple of 32."""
+    g = np.random.default_rng(4)
+    for max_seq, cuts in ((100, (100, 99, 96, 95, 33)), (2000, (2000, 1985, 1984, 1950, 1100))):
+        k, v = (normal(g, 2, 2, max_seq, 64).bfloat16() for _ in range(2))
+        rows = Rows(k, v, [max_seq, max_seq])
+        for cut in cuts:
+            rows.check(normal(g, 2, 4, 64), [2 ** 31 - 1, -2 ** 31], cut, keys=[cut, 0])
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("max_seq", [300, 2300])
+def test_any_slots_of_rows_of_known_lengths(dim, max_seq):
+    """Every kind of prefix; positions and max_ctx beyond the length stop at it. What is not attended to may be anything."""
+    g = np.random.default_rng(max_seq + dim)
+    lengths = [max_seq, max_seq // 32 * 32, 257, 31, 0]
+    k, v = (normal(g, 5, 2, max_seq, dim).bfloat16() for _ in range(2))
+    k[:, :, 96:128] = 0                                      # a block of zero keys, some of them cut off
+    rows = Rows(k, v, lengths)
+    for tail in (rows.cache.k_tail, rows.cache.v_tail):
+        for r, n in enumerate(lengths):
+            tail[:, r, :, n % BLOCK:] = float("nan")
+    for at in ([max_seq - 1] * 5, [250, 100, 255, 30, 0], [255, 96, 256, 0, -1], [0, 31, 32, 40, 7], [-1, 97, 257, -9, 2 ** 31 - 1],
+               [126, 127, 128, 5, 5], [max_seq - 2, max_seq - 45, 224, 8, 0]):
+        for max_ctx in (max_seq, max_seq - 37, 101):
+            keys = [max(0, min(p + 1, n, max_ctx)) for p, n in zip(at, lengths)]
+            q = normal(g, 5, 6, dim)
+            rows.check(q, at, max_ctx, keys=keys, lengths=i32(lengths))
+            q[:, :] = 0
+            rows.check(q, at, max_ctx, keys=keys, lengths=i32(lengths))
+
+
+def test_a_bad_block_behind_the_cut_is_not_seen():
+    g = np.random.default_rng(5)
+    for n, cut in ((320, 200), (2400, 2200)):
+        k, v = (normal(g, 1, 1, n, 64) for _ in range(2))
+        k[0, 0, cut // BLOCK * BLOCK + BLOCK] = float("nan")
+        v[0, 0, cut // BLOCK * BLOCK + BLOCK + 1] = float("inf")
+        rows = Rows(k.bfloat16(), v.bfloat16(), [cut // BLOCK * BLOCK + BLOCK])   # what is attended to, as it is held
+        rows.cache.append(k[None].bfloat16().cuda(), v[None].bfloat16().cuda(), i32([0]))
+        rows.check(normal(g, 1, 4, 64), [n - 1], cut, keys=[cut])
+        rows.check(normal(g, 1, 4, 64), [cut - 1], n, keys=[cut], lengths=i32([n]))
+
+
+def test_lengths_on_the_host_or_too_few_are_refused():
+    cache = QCache(ModelConfig("shape", 1, 512, 1, 1, 64, 1024, 4096), 2, 64)
+    q, out = torch.zeros(2, 4, 64, device="cuda"), torch.full((2, 4, 64), 7.0, device="cuda")
+    for bad in (torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32, device="cuda"),
+                torch.zeros(2, dtype=torch.int64, device="cuda")):
+        with pytest.raises(AssertionError, match="lengths"):
+            cache.attention(0, q, i32([0, 0]), out, lengths=bad)
+    torch.cuda.synchronize()
+    assert torch.all(out == 7)

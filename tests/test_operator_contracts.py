@@ -1,0 +1,28 @@
+"""Contracts of beam selection, reordering and the 8-bit cache that hold on the host, before anything is enqueued: calls
+that are refused (no pointer is followed), and what the binding checks. No GPU is needed."""
+import ctypes
+
+import pytest
+
+from persistent_megakernel_interpreter_b200 import _lib
+
+OK, INVALID, UNSUPPORTED = 0, 1, 3
+PTR = ctypes.c_void_p(4096)
+
+
+def qcache(**kw):
+    a = dict(n_layers=2, max_batch=4, n_kv_heads=2, max_seq=2048, head_dim=64, reserved0=0, k_codes=4096, v_codes=4096,
+             k_scale=4096, v_scale=4096, k_tail=4096, v_tail=4096)
+    a.update(kw)
+    return ctypes.byref(_lib.MkQcache(*a.values()))
+
+
+@pytest.mark.parametrize("kw, code", [
+    (dict(lengths=None), INVALID), (dict(positions=None), INVALID), (dict(q=None), INVALID), (dict(out=None), INVALID),
+    (dict(layer=2), INVALID), (dict(rows=5), INVALID), (dict(max_ctx=2049), INVALID), (dict(n_heads=10), UNSUPPORTED),
+    (dict(max_ctx=2048), INVALID), (dict(cache=dict(head_dim=32)), UNSUPPORTED)])
+def test_attention_of_a_prefix_refuses(kw, code):
+    a = dict(cache={}, layer=0, rows=2, n_heads=4, max_ctx=64, q=PTR, positions=PTR, lengths=PTR, out=PTR, work=None, size=0)
+    a.update(kw)
+    a["cache"] = qcache(**a["cache"])
+    assert _lib.lib().mk_qcache_attention_prefix(*a.values(), None) == code
