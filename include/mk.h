@@ -222,6 +222,10 @@ mk_status mk_decode_step_host(mk_handle* h, const int32_t* tokens_host,
  * step is skipped until this call clears it. Returns MK_ERR_CUDA if the sync fails. */
 mk_status mk_get_status(mk_handle* h, mk_status* device_status, char* msg, size_t msg_len);
 
+/* The device int32 that holds what mk_get_status would report, for kernels that go by it; valid until the
+ * handle's next mk_build_schedule or mk_destroy. NULL for a NULL handle and before mk_build_schedule. */
+const int32_t* mk_device_status(mk_handle* h);
+
 /* Frees everything the handle owns. NULL is allowed. */
 void mk_destroy(mk_handle* h);
 
@@ -283,6 +287,14 @@ mk_status mk_beam_select(const float* logits, int64_t row_stride, int batch, int
                          const float* scores, const int32_t* finished, int32_t eos, int32_t* next_tokens,
                          int32_t* parents, float* next_scores, int32_t* next_finished, int32_t* positions,
                          void* stream);
+
+/* The same behind a step that may have failed: where *status (device int32, read when the call runs) is not
+ * MK_OK, nothing is chosen; every parent is -1, which mk_cache_reorder and mk_qcache_reorder leave alone, and
+ * the other outputs and the positions stay as they are. status: a step's status_out, or mk_device_status(). */
+mk_status mk_beam_select_checked(const float* logits, int64_t row_stride, int batch, int beams, int vocab, int n_out,
+                                 const float* scores, const int32_t* finished, int32_t eos, int32_t* next_tokens,
+                                 int32_t* parents, float* next_scores, int32_t* next_finished, int32_t* positions,
+                                 const int32_t* status, void* stream);
 
 /* Rows of a KV cache take over other rows' slots, all at once and in place: for each row r < rows,
  * layer and head, slots starts[r] <= s < lengths[parents[r]] of row r become those of row parents[r]

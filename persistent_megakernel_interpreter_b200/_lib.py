@@ -120,6 +120,9 @@ def lib() -> ctypes.CDLL:
                                            ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)]
     i = ctypes.c_int
     L.mk_beam_select.argtypes = [P, ctypes.c_int64, i, i, i, i, P, P, I32, P, P, P, P, P, P]
+    L.mk_beam_select_checked.argtypes = [P, ctypes.c_int64, i, i, i, i, P, P, I32, P, P, P, P, P, P, P]
+    L.mk_device_status.argtypes = [P]
+    L.mk_device_status.restype = P
     L.mk_cache_reorder.argtypes = [ctypes.POINTER(MkConfig), P, P, i, P, P, P, P]
     qc = ctypes.POINTER(MkQcache)
     L.mk_qcache_append.argtypes = [qc, i, i, i, i, P, P, ctypes.POINTER(ctypes.c_int64), P, P, P]
@@ -135,7 +138,7 @@ def lib() -> ctypes.CDLL:
               "mk_decode_step_host", "mk_get_status", "mk_plan_schedule_host",
               "mk_get_schedule_info", "mk_read_counters", "mk_pack_weights_host", "mk_read_trace",
               "mk_baseline_decode_step_noalloc", "mk_greedy_select", "mk_tensor_map_specs_host",
-              "mk_beam_select", "mk_cache_reorder", "mk_qcache_append", "mk_qcache_reorder", "mk_qcache_attention",
+              "mk_beam_select", "mk_beam_select_checked", "mk_cache_reorder", "mk_qcache_append", "mk_qcache_reorder", "mk_qcache_attention",
               "mk_qcache_attention_prefix", "mk_decode_step_qcache"):
         getattr(L, f).restype = st
     _lib = L

@@ -619,6 +619,10 @@ extern "C" mk_status mk_decode_step_qcache(mk_handle* h, const mk_qcache* c, int
     return mk::qcache_step_launch(s, static_cast<cudaStream_t>(stream), h->dev_sms);
 }
 
+extern "C" const int32_t* mk_device_status(mk_handle* h) {
+    return h && h->ctl ? reinterpret_cast<const int32_t*>(&h->ctl->status) : nullptr;
+}
+
 extern "C" mk_status mk_get_status(mk_handle* h, mk_status* device_status, char* msg,
                                    size_t msg_len) {
     if (!h) return MK_ERR_INVALID_ARG;

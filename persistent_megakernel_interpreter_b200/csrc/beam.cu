@@ -57,6 +57,7 @@ struct BeamArgs {
     float* next_scores;
     int32_t* next_finished;
     int32_t* positions;
+    const int32_t* status;               // NULL, or where it is not 0 nothing is chosen
 };
 
 struct Cand {
@@ -348,6 +349,11 @@ __global__ void __launch_bounds__(T, 1024 / T) k_beam_select(const __grid_consta
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int b = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31;
     cudaGridDependencySynchronize();           // everything enqueued before has run
+    if (a.status && *a.status != 0) {          // the same for every CTA: none waits for another
+        const unsigned per = cluster.num_blocks(), at = blockIdx.x / per * a.n_out + threadIdx.x;
+        if (blockIdx.x % per == 0 && threadIdx.x < a.n_out) a.parents[at] = -1;
+        return;
+    }
     auto running = cluster.barrier_arrive();   // waited for before another CTA's shared memory is written
     BeamSmem* head = cluster.map_shared_rank(&sm, 0);
     const int n = min(a.n_out, a.vocab);
@@ -488,10 +494,11 @@ cudaError_t launch_beam(const BeamArgs& a, int C, cudaStream_t st) {
 }  // namespace
 }  // namespace mk
 
-extern "C" mk_status mk_beam_select(const float* logits, int64_t row_stride, int batch, int beams, int vocab, int n_out,
-                                    const float* scores, const int32_t* finished, int32_t eos, int32_t* next_tokens,
-                                    int32_t* parents, float* next_scores, int32_t* next_finished, int32_t* positions,
-                                    void* stream) {
+namespace mk {
+static mk_status beam_select(const float* logits, int64_t row_stride, int batch, int beams, int vocab, int n_out,
+                             const float* scores, const int32_t* finished, int32_t eos, int32_t* next_tokens,
+                             int32_t* parents, float* next_scores, int32_t* next_finished, int32_t* positions,
+                             const int32_t* status, void* stream) {
     if (!logits || !scores || !next_tokens || !parents || !next_scores) return MK_ERR_INVALID_ARG;
     if (batch < 1 || beams < 1 || vocab < 1 || n_out < 1 || row_stride < vocab) return MK_ERR_INVALID_ARG;
     if (beams > mk::kMaxBeams || n_out > mk::kMaxOut || vocab > (1 << 24) || batch > (1 << 20)) return MK_ERR_UNSUPPORTED;
@@ -514,6 +521,7 @@ extern "C" mk_status mk_beam_select(const float* logits, int64_t row_stride, int
     a.next_scores = next_scores;
     a.next_finished = next_finished;
     a.positions = positions;
+    a.status = status;
     // CTAs per sequence. Few sequences with long rows or many beams take 16 (2 x 4 rows of 128256: 9.0 us against 11
     // with 8); a moderate number at least 8 (8 rows of 128256: 7.7 us, 11.4 with 16; 32 x 8 of 50257: 17,
     // 29 with 16); from there on a CTA takes a whole row (64 x 4 of 32000: 12.0 us, 20.3 with 8), of many sequences
@@ -530,4 +538,23 @@ extern "C" mk_status mk_beam_select(const float* logits, int64_t row_stride, int
                           : tokens >= 6144 ? mk::launch_beam<256>(a, C, st)
                                            : mk::launch_beam<128>(a, C, st);
     return e == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+}
+}  // namespace mk
+
+extern "C" mk_status mk_beam_select(const float* logits, int64_t row_stride, int batch, int beams, int vocab, int n_out,
+                                    const float* scores, const int32_t* finished, int32_t eos, int32_t* next_tokens,
+                                    int32_t* parents, float* next_scores, int32_t* next_finished, int32_t* positions,
+                                    void* stream) {
+    return mk::beam_select(logits, row_stride, batch, beams, vocab, n_out, scores, finished, eos, next_tokens, parents,
+                           next_scores, next_finished, positions, nullptr, stream);
+}
+
+extern "C" mk_status mk_beam_select_checked(const float* logits, int64_t row_stride, int batch, int beams, int vocab,
+                                            int n_out, const float* scores, const int32_t* finished, int32_t eos,
+                                            int32_t* next_tokens, int32_t* parents, float* next_scores,
+                                            int32_t* next_finished, int32_t* positions, const int32_t* status,
+                                            void* stream) {
+    if (!status) return MK_ERR_INVALID_ARG;
+    return mk::beam_select(logits, row_stride, batch, beams, vocab, n_out, scores, finished, eos, next_tokens, parents,
+                           next_scores, next_finished, positions, status, stream);
 }

@@ -112,9 +112,10 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t wanted, F&& body) {
 constexpr c10::ScalarType kI32 = c10::ScalarType::Int, kF32 = c10::ScalarType::Float, kBf16 = c10::ScalarType::BFloat16,
                           kU8 = c10::ScalarType::Byte;
 
-// logits, scores, next_tokens, parents, next_scores, finished, eos, next_finished, positions, stream
+// logits, scores, next_tokens, parents, next_scores, finished, eos, next_finished, positions, stream[, status: a tensor
+// or a device address]
 PyObject* beam_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 10, [&] {
+    return guarded(n, n == 11 ? 11 : 10, [&] {
         const at::Tensor &logits = tensor(a[0], "logits"), &scores = tensor(a[1], "scores"), &tokens = tensor(a[2], "next_tokens");
         const int device = device_of(logits, "logits");
         check(logits, "logits", kF32, device);
@@ -135,9 +136,19 @@ PyObject* beam_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
         int32_t* next_fin = at_least_or_null<int32_t>(a[7], "next_finished", kI32, n_all, device);
         int32_t* pos = at_least_or_null<int32_t>(a[8], "positions", kI32, n_in, device);
         void* stream = stream_of(a[9], device);
+        const int32_t* status = nullptr;
+        if (n == 11 && PyLong_Check(a[10])) {
+            status = static_cast<const int32_t*>(PyLong_AsVoidPtr(a[10]));
+            if (!status) refuse("status", "an address is wanted");
+        } else if (n == 11) {
+            status = at_least_or_null<int32_t>(a[10], "status", kI32, 1, device);
+        }
         const float* x = static_cast<const float*>(logits.data_ptr());
         const int64_t stride = rows > 1 ? logits.stride(0) : vocab;
         return unlocked([&] {
+            if (status)
+                return mk_beam_select_checked(x, stride, (int)batch, (int)beams, (int)vocab, (int)n_out, sc, fin, eos, tok, par, out,
+                                              next_fin, pos, status, stream);
             return mk_beam_select(x, stride, (int)batch, (int)beams, (int)vocab, (int)n_out, sc, fin, eos, tok, par, out, next_fin, pos,
                                   stream);
         });

@@ -153,7 +153,7 @@ class Megakernel:
 
     def decode_steps_beam(self, tokens, positions, cache, logits, scores, n_steps: int, finished=None, eos: int = -1,
                           starts=None, generated=None, parents=None, max_ctx: int | None = None, workspace=None,
-                          stream=None) -> None:
+                          stream=None, status=None) -> None:
         """``n_steps`` beam-search steps with no host work between them. ``scores`` (fp32
         [sequences][beams]) says how the batch's rows are grouped; each step decodes every row, picks
         each sequence's best ``beams`` continuations (``beam_select``) into ``tokens``, ``scores`` and
@@ -161,11 +161,18 @@ class Megakernel:
         (k_cache, v_cache) for ``decode_step``, or a ``qcache.QCache`` for ``decode_step_qcache`` (which
         takes ``max_ctx`` and ``workspace``). ``starts`` (int32 [rows]): slots below are the same in
         all beams of a sequence (the prompt). ``generated`` and ``parents`` (int32 [n_steps][rows],
-        optional) receive each step's tokens and the rows they continue."""
+        optional) receive each step's tokens and the rows they continue.
+
+        Every row's positions advance, a finished one's too, so positions + n_steps may not pass
+        max_ctx for any row. A step that fails (a position at the end, a bad token) ends the search
+        there: from it on nothing is stored, chosen or moved, tokens, positions and scores are those
+        of the step before, and its and the later steps' ``parents`` are -1. On an 8-bit cache
+        ``status`` (int32 [1], optional) receives its code, or 0; on a bf16 cache ``status()`` reports it."""
         from .qcache import QCache
         rows = tokens.numel()
         assert scores.dim() == 2 and scores.numel() == rows
         assert isinstance(cache, QCache) or self.batch == rows, "the schedule is built for another batch"
+        assert isinstance(cache, QCache) or status is None, "status() reports the steps on a bf16 cache"
         for t in (generated, parents):
             assert t is None or (t.dtype == torch.int32 and t.is_contiguous() and t.numel() >= n_steps * rows)
         s = stream or torch.cuda.current_stream()
@@ -175,14 +182,19 @@ class Megakernel:
                 max_ctx = min(cache.max_seq, self.max_seq) if max_ctx is None else max_ctx
                 if workspace is None:
                     workspace = self.decode_step_qcache_workspace(cache, rows, max_ctx)
+                if status is None:
+                    status = torch.empty(1, dtype=torch.int32, device=tokens.device)
+            else:
+                status = _lib.lib().mk_device_status(self._h)
         for i in range(n_steps):
             to = came if parents is None else parents.view(-1)[i * rows:(i + 1) * rows]
             if isinstance(cache, QCache):
-                self.decode_step_qcache(tokens, positions, cache, logits, max_ctx=max_ctx, workspace=workspace, stream=s)
+                self.decode_step_qcache(tokens, positions, cache, logits, max_ctx=max_ctx, workspace=workspace, status=status,
+                                        stream=s)
             else:
                 self.decode_step(tokens, positions, cache[0], cache[1], logits, stream=s)
             beam_select(logits.view(rows, -1), scores, tokens.view_as(scores), to.view_as(scores), scores,
-                        finished=finished, eos=eos, next_finished=finished, positions=positions, stream=s)
+                        finished=finished, eos=eos, next_finished=finished, positions=positions, stream=s, status=status)
             if isinstance(cache, QCache):
                 cache.reorder(to, positions, starts=starts, stream=s)
             else:
@@ -243,7 +255,7 @@ def greedy_select(logits: torch.Tensor, next_tokens: torch.Tensor, positions=Non
 
 def beam_select(logits: torch.Tensor, scores: torch.Tensor, next_tokens: torch.Tensor, parents: torch.Tensor,
                 next_scores: torch.Tensor, finished=None, eos: int = -1, next_finished=None, positions=None,
-                stream=None) -> None:
+                stream=None, status=None) -> None:
     """The best continuations of every sequence's beams, on the device and asynchronous on ``stream``.
 
     ``logits`` fp32 [sequences * beams][vocab] (rows may be strided), ``scores`` fp32
@@ -252,9 +264,10 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, next_tokens: torch.T
     log_softmax(logits). A beam with a nonzero ``finished`` (int32 [sequences][beams]) goes on with
     ``eos`` at its own score; ``next_finished`` receives who is finished then. ``positions``
     (optional, one per row) are advanced by one. ``next_scores`` may be ``scores`` and
-    ``next_finished`` may be ``finished``."""
+    ``next_finished`` may be ``finished``. ``status`` (int32 [1], optional): the status of the step that the
+    logits come from; where it is not 0 nothing is chosen: the parents are -1 and all else stays as it is."""
     _lib.check(_lib.call().beam_select(logits, scores, next_tokens, parents, next_scores, finished, eos, next_finished,
-                                       positions, stream), "mk_beam_select")
+                                       positions, stream, status), "mk_beam_select")
 
 
 def cache_reorder(k_cache: torch.Tensor, v_cache: torch.Tensor, parents: torch.Tensor, lengths: torch.Tensor,

@@ -26,3 +26,10 @@ def test_attention_of_a_prefix_refuses(kw, code):
     a.update(kw)
     a["cache"] = qcache(**a["cache"])
     assert _lib.lib().mk_qcache_attention_prefix(*a.values(), None) == code
+
+
+def test_a_checked_selection_refuses_without_a_status():
+    def call(logits, status):
+        return _lib.lib().mk_beam_select_checked(logits, 100, 1, 2, 100, 2, PTR, None, -1, PTR, PTR, PTR, None, None, status, None)
+    assert call(PTR, None) == INVALID and call(None, PTR) == INVALID
+    assert _lib.lib().mk_device_status(None) is None
