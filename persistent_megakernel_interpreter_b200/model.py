@@ -171,6 +171,7 @@ class Megakernel:
         from .qcache import QCache
         rows = tokens.numel()
         assert scores.dim() == 2 and scores.numel() == rows
+        assert logits.numel() >= rows * self.cfg.vocab, "a row of logits for each row of the batch is wanted"
         assert isinstance(cache, QCache) or self.batch == rows, "the schedule is built for another batch"
         assert isinstance(cache, QCache) or status is None, "status() reports the steps on a bf16 cache"
         for t in (generated, parents):
@@ -186,6 +187,7 @@ class Megakernel:
                     status = torch.empty(1, dtype=torch.int32, device=tokens.device)
             else:
                 status = _lib.lib().mk_device_status(self._h)
+        chosen_from = logits.view(-1)[:rows * self.cfg.vocab].view(rows, -1)
         for i in range(n_steps):
             to = came if parents is None else parents.view(-1)[i * rows:(i + 1) * rows]
             if isinstance(cache, QCache):
@@ -193,7 +195,7 @@ class Megakernel:
                                         stream=s)
             else:
                 self.decode_step(tokens, positions, cache[0], cache[1], logits, stream=s)
-            beam_select(logits.view(rows, -1), scores, tokens.view_as(scores), to.view_as(scores), scores,
+            beam_select(chosen_from, scores, tokens.view_as(scores), to.view_as(scores), scores,
                         finished=finished, eos=eos, next_finished=finished, positions=positions, stream=s, status=status)
             if isinstance(cache, QCache):
                 cache.reorder(to, positions, starts=starts, stream=s)

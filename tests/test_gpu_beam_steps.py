@@ -154,3 +154,19 @@ def test_a_captured_search_stops_when_a_replay_reaches_the_end():
     assert all(torch.equal(x, y) for x, y in zip(s.state(), t.state()))
     s.mk.close()
     t.mk.close()
+
+
+@pytest.mark.parametrize("kind", ["8-bit", "bf16"])
+def test_logits_of_a_larger_batch(kind):
+    """A buffer with room for more rows than the step has (one for max_batch, say) gives the same search."""
+    a, b = Search(kind, past=(10, 12)), Search(kind, past=(10, 12))
+    b.logits = torch.full((7, TINY.vocab), 50.0, device="cuda")
+    want, got = a.run(5), b.run(5)
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    assert all(torch.equal(x, y) for x, y in zip(a.state(), b.state()))
+    assert torch.equal(a.logits, b.logits[:4]) and torch.all(b.logits[4:] == 50)
+    b.logits = b.logits[:3]
+    with pytest.raises(AssertionError):
+        b.run(1)
+    a.mk.close()
+    b.mk.close()
