@@ -125,9 +125,13 @@ class Megakernel:
         self._step(_lib.lib().mk_baseline_decode_step, tokens, positions, k_cache, v_cache, logits,
                    stream)
 
+    def _check_device(self, cache) -> None:
+        assert cache._device == self.device, f"the cache is on cuda:{cache._device}, the model on cuda:{self.device}"
+
     def decode_step_qcache_workspace(self, cache, batch: int, max_ctx: int) -> torch.Tensor:
         """A workspace for ``decode_step_qcache`` calls of this size. Calls that may overlap on the GPU
         need one each."""
+        self._check_device(cache)
         n = _lib.lib().mk_decode_step_qcache_workspace(self._h, cache._ref, batch, max_ctx)
         if n == 0:
             raise _lib.MkError(1, "mk_decode_step_qcache_workspace")
@@ -138,6 +142,7 @@ class Megakernel:
         """One step as ordinary kernels on an 8-bit cache (``qcache.QCache``); it needs no schedule, and
         contexts may be as long as the cache. ``status`` (int32 [1], optional) receives the step's
         device status. Without a ``workspace`` one is allocated for the call."""
+        self._check_device(cache)
         device = torch.cuda.current_device()
         batch = tokens.numel()
         max_ctx = min(cache.max_seq, self.max_seq) if max_ctx is None else max_ctx

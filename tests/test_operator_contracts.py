@@ -33,3 +33,27 @@ def test_a_checked_selection_refuses_without_a_status():
         return _lib.lib().mk_beam_select_checked(logits, 100, 1, 2, 100, 2, PTR, None, -1, PTR, PTR, PTR, None, None, status, None)
     assert call(PTR, None) == INVALID and call(None, PTR) == INVALID
     assert _lib.lib().mk_device_status(None) is None
+
+
+def test_a_cache_on_another_device_than_the_model_is_refused(monkeypatch):
+    """Before the library is called or anything is allocated: its pointers would be followed on the wrong device."""
+    from types import SimpleNamespace
+    import torch
+    from persistent_megakernel_interpreter_b200.config import TINY
+    from persistent_megakernel_interpreter_b200.model import Megakernel
+    mk = Megakernel.__new__(Megakernel)
+    mk._h, mk.device, mk.cfg, mk.max_seq = None, 0, TINY, 64
+    cache = SimpleNamespace(_device=1, _ref=None, max_seq=64)
+
+    def called(*a):
+        raise RuntimeError("reached")
+    monkeypatch.setattr(_lib, "lib", lambda: SimpleNamespace(mk_decode_step_qcache=called, mk_decode_step_qcache_workspace=called))
+    x = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(AssertionError, match="cuda:1"):
+        mk.decode_step_qcache_workspace(cache, 1, 64)
+    for ws in (None, x):
+        with pytest.raises(AssertionError, match="cuda:1"):
+            mk.decode_step_qcache(x, x, cache, x, workspace=ws)
+    cache._device = 0
+    with pytest.raises(RuntimeError, match="reached"):
+        mk.decode_step_qcache_workspace(cache, 1, 64)
