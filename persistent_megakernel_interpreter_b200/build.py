@@ -1,5 +1,6 @@
 """Build libmk.so in-tree with nvcc for sm_100a (no JIT, no torch in it), and _call.so,
-the compiled part of the Python binding, with g++ against torch's headers.
+the compiled part of the Python binding, with g++ against torch's headers (left out where
+torch is not installed: the library does not need it).
 
 ``python -m persistent_megakernel_interpreter_b200.build`` or ``build_library()``.
 """
@@ -42,7 +43,11 @@ def _call_stale() -> bool:
 
 def _build_call(verbose: bool) -> None:
     """Compile the binding against torch's headers; it links to libmk.so beside it."""
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        print("torch is not installed: _call.so, the compiled part of the Python binding, is not built", file=sys.stderr)
+        return
+    torch = spec.submodule_search_locations[0]
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
     tmp = f"{CALL}.tmp{os.getpid()}"
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-I{INCLUDE}",
