@@ -23,6 +23,7 @@ SOURCES = ["api.cu", "megakernel.cu", "megakernel_trace.cu", "baseline.cu", "noa
            "reorder.cu", "qcache.cu", "pack.cpp", "schedule.cpp"]
 HEADERS = ["mk_internal.h", "mk_device.cuh", "pack.h", "qcache.h"]
 CALL = os.path.join(PKG, "_call.so")
+CALL_STAMP = os.path.join(PKG, "_call.stamp")   # what _call.so was built against
 CALL_SOURCE = os.path.join(CSRC, "binding.cpp")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -34,20 +35,35 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def _torch_dir() -> str | None:
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec is not None else None
+
+
+def _call_stamp(torch: str) -> str:
+    """The Python and the torch that the binding's machine code belongs to."""
+    with open(os.path.join(torch, "version.py")) as f:
+        return sys.version + "\n" + f.read()
+
+
 def _call_stale() -> bool:
-    if not os.path.exists(CALL):
+    torch = _torch_dir()
+    if not os.path.exists(CALL) or not os.path.exists(CALL_STAMP):
         return True
+    if torch is not None:
+        with open(CALL_STAMP) as f:
+            if f.read() != _call_stamp(torch):
+                return True
     t = os.path.getmtime(CALL)
     return any(os.path.getmtime(d) > t for d in (CALL_SOURCE, os.path.join(INCLUDE, "mk.h"), os.path.abspath(__file__)))
 
 
 def _build_call(verbose: bool) -> None:
     """Compile the binding against torch's headers; it links to libmk.so beside it."""
-    spec = importlib.util.find_spec("torch")
-    if spec is None:
+    torch = _torch_dir()
+    if torch is None:
         print("torch is not installed: _call.so, the compiled part of the Python binding, is not built", file=sys.stderr)
         return
-    torch = spec.submodule_search_locations[0]
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
     tmp = f"{CALL}.tmp{os.getpid()}"
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-I{INCLUDE}",
@@ -59,6 +75,8 @@ def _build_call(verbose: bool) -> None:
     try:
         subprocess.check_call(cmd)
         os.replace(tmp, CALL)
+        with open(CALL_STAMP, "w") as f:
+            f.write(_call_stamp(torch))
     finally:
         if os.path.exists(tmp):
             os.remove(tmp)
