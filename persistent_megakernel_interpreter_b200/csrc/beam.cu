@@ -401,7 +401,9 @@ __global__ void __launch_bounds__(T, 1024 / T) k_beam_select(const __grid_consta
         float m = -INFINITY, s = 0.f;
         for (int j = 0; j < splits; ++j) m = fmaxf(m, sm.m[p0 + j]);
         const float ref = finite(m);
-        for (int j = 0; j < splits; ++j) s = fmaf(sm.s[p0 + j], e2((finite(sm.m[p0 + j]) - ref) * kLog2E), s);
+        // beside an infinite maximum only the pieces that have one count: their sums are its numbers
+        for (int j = 0; j < splits; ++j)
+            s = fmaf(sm.s[p0 + j], m == INFINITY ? (float)(sm.m[p0 + j] == INFINITY) : e2((finite(sm.m[p0 + j]) - ref) * kLog2E), s);
         sm.m_row[k] = m;
         sm.log_row[k] = log((double)s);
     }

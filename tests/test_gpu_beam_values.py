@@ -1,0 +1,45 @@
+"""Beam selection where the logits are not the ordinary ones, against the plain 64-bit form: tokens and parents are exact; a
+score is off by at most the fp32 sum's rounding, (vocab / 512 + 64) 2^-24 + 17 * 2^-23 + 2^-21 in its logarithm, and 2^-24 of
+its magnitude."""
+import numpy as np
+import pytest
+import torch
+
+from cases_beam_cache import select
+from persistent_megakernel_interpreter_b200.model import beam_select
+
+pytestmark = pytest.mark.gpu
+
+BIG = np.finfo(np.float32).max
+
+
+def check(x, scores, n_out):
+    tok, par, tot, _ = select(x, scores, n_out)
+    got = [torch.full((scores.shape[0], n_out), -7, dtype=torch.int32, device="cuda") for _ in range(2)]
+    got.append(torch.full((scores.shape[0], n_out), 7.0, device="cuda"))
+    beam_select(torch.from_numpy(x).cuda(), torch.from_numpy(scores).cuda(), *got)
+    torch.cuda.synchronize()
+    t, p, s = (g.cpu().numpy() for g in got)
+    assert np.array_equal(t, tok) and np.array_equal(p, par)
+    ends = np.isfinite(tot)
+    assert np.array_equal(s[~ends], tot[~ends].astype(np.float32))
+    tol = (x.shape[1] / 512 + 64) * 2.0 ** -24 + 17 * 2.0 ** -23 + 2.0 ** -21 + np.abs(tot[ends]) * 2.0 ** -24
+    assert np.all(np.abs(s[ends] - tot[ends]) <= tol)
+
+
+@pytest.mark.parametrize("batch, beams, vocab", [(1, 1, 128256), (2, 4, 128256), (1, 4, 4096), (40, 4, 1000), (3, 16, 300)])
+def test_infinite_logits_beside_the_largest_number(batch, beams, vocab):
+    """The infinite ones share their row among themselves, wherever the row is cut."""
+    g = np.random.default_rng(vocab)
+    x = g.standard_normal((batch * beams, vocab)).astype(np.float32)
+    scores = np.zeros((batch, beams), np.float32)
+    for r in range(batch * beams):
+        x[r, g.choice(vocab, 40, replace=False)] = BIG
+        x[r, g.choice(vocab, 1 + r % 3, replace=False)] = np.inf
+    check(x, scores, min(8, vocab))
+    x[:, vocab // 2:] = BIG                                  # half of each row
+    x[:, 1] = np.inf
+    check(x, scores, min(8, vocab))
+    x[:, 1] = -np.inf                                        # and without infinities
+    x[np.isposinf(x)] = BIG
+    check(x, scores, min(8, vocab))
