@@ -174,6 +174,7 @@ __host__ __device__ constexpr int attn_stages(int hd) { return hd == 64 ? 3 : 2;
 __host__ __device__ constexpr int attn_per_sm(int hd) { return hd == 64 ? 2 : 3; }
 constexpr int kHalf = 4096;            // bytes of a batch's keys, and of its values
 __host__ __device__ constexpr int batch_blocks(int hd) { return hd == 64 ? 2 : 1; }
+constexpr float kLowest = -3.402823466e38f;   // maxima are finite: a difference of two is a number or an infinity
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnArgs {
@@ -378,7 +379,7 @@ __device__ __forceinline__ void attn_blocks(const AttnArgs& a, AttnSmem<HD>& sm,
     // lanes of odd t read the two keys of a pair in the other order at 64 dims (other banks)
     const bool odd = HD == 64 && (t & 1);
     const uint32_t sel_lo = odd ? 0x1504u : 0x5140u, sel_hi = odd ? 0x3726u : 0x7362u;
-    float M = -1e30f, l = 0.f, o[VD][2];
+    float M = kLowest, l = 0.f, o[VD][2];
 #pragma unroll
     for (int i = 0; i < VD; ++i) o[i][0] = o[i][1] = 0.f;
     const int b1 = src.b1;
@@ -396,9 +397,7 @@ __device__ __forceinline__ void attn_blocks(const AttnArgs& a, AttnSmem<HD>& sm,
         for (int b = 0; b < BB; ++b) {
             // the block's keys that count, from the lane's first on (of the 32 that are its own and its pair's)
             left[b] = src.keys - (blk + b) * kQBlock - 2 * t - up;
-            // never zero: what a key behind the last gets, -infinity, has to stay that
-            ks[b] = b == 0 || blk + b < b1 ? sm.scale[warp][stage][0][b] * kmul : 1.0f;
-            ks[b] = ks[b] == 0.f ? 1e-38f : ks[b];
+            ks[b] = sm.scale[warp][stage][0][b] * kmul;
             vs[b] = __float_as_uint(sm.scale[warp][stage][1][b]);
             ev[b] = max((int)(vs[b] >> 23) - 127, kLeastScale);
         }
@@ -419,13 +418,14 @@ __device__ __forceinline__ void attn_blocks(const AttnArgs& a, AttnSmem<HD>& sm,
             const float f0 = sum_of(acc[0], sm0) + sum_of(acc[2], sm1), f1 = sum_of(acc[1], sm0) + sum_of(acc[3], sm1);
             s[n] = (up ? f1 : f0) + __shfl_xor_sync(0xffffffffu, up ? f0 : f1, 16);
             const int b = n / (kQBlock / 8);
-            if (8 * (n % (kQBlock / 8)) >= left[b]) s[n] = -INFINITY;
-            most[b] = fmaxf(most[b], s[n] * ks[b]);
+            // rounded here, like a sum of its products, and so the same number in the maximum and in the weight
+            s[n] = 8 * (n % (kQBlock / 8)) < left[b] ? s[n] * ks[b] : -INFINITY;
+            most[b] = fmaxf(most[b], s[n]);
         }
         float top = -INFINITY;
 #pragma unroll
         for (int b = 0; b < BB; ++b) {
-            most[b] = fmaxf(ceilf(most[b]), -1e30f);
+            most[b] = fmaxf(ceilf(most[b]), kLowest);
             top = fmaxf(top, most[b] + (float)ev[b]);
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -446,7 +446,7 @@ __device__ __forceinline__ void attn_blocks(const AttnArgs& a, AttnSmem<HD>& sm,
             float sum = 0.f;
 #pragma unroll
             for (int n = b * (kQBlock / 8); n < (b + 1) * (kQBlock / 8); ++n) {
-                const float w = ex2(fmaf(s[n], ks[b], -most[b]));
+                const float w = ex2(s[n] - most[b]);
                 sum += w;
                 const uint32_t W = __float2uint_rn(w * vm);
                 wp[n] = __byte_perm(W, __shfl_xor_sync(0xffffffffu, W, 16), sel_w);
@@ -564,7 +564,7 @@ __device__ __forceinline__ void AttnTail<HD>::attend(AttnSmem<HD>& sm, int n, in
     float m = s;
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-    m = fmaxf(ceilf(m), -1e30f);             // e = 0
+    m = fmaxf(ceilf(m), kLowest);             // e = 0
     const float w = lane < n ? exp2f(s - m) : 0.f;
     float l = w;
 #pragma unroll
@@ -874,7 +874,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_merge_q(const __grid_c
                 const float2 x = *reinterpret_cast<const float2*>(a.part_o + at(k) * HD + lane * D);
                 p[k][0] = x.x;
                 p[k][1] = x.y;
-                if (i + k >= total) ml[k] = make_float2(-INFINITY, 0.f);   // a partial's maximum is never below -1e30
+                if (i + k >= total) ml[k] = make_float2(-INFINITY, 0.f);   // a partial's maximum is a number
             }
             float Mn = M;
 #pragma unroll

@@ -171,3 +171,31 @@ def test_lengths_on_the_host_or_too_few_are_refused():
             cache.attention(0, q, i32([0, 0]), out, lengths=bad)
     torch.cuda.synchronize()
     assert torch.all(out == 7)
+
+
+# ------------------------------------------------------------------ scores far from the ordinary ones
+
+def check_one_sided(dim, n, good, bad, query, seed):
+    """Keys of one dim only, `good` for a third of them and `bad` for the others, and queries `query` there. A score x moves by up
+    to 2^-22 |x| on its way to a weight, which beyond 2^22 says nothing of the good keys' shares any more; but the bad ones, a
+    third of x away, have none. So an output is finite and lies among the good keys' values."""
+    g = np.random.default_rng(seed)
+    k, v = torch.zeros(1, 1, n, dim), normal(g, 1, 1, n, dim).bfloat16()
+    best = g.permutation(n) < (n + 2) // 3
+    k[0, 0, :, 0] = torch.from_numpy(np.where(best, good, bad).astype(np.float32))
+    rows = Rows(k.bfloat16(), v, [n])
+    q, out = torch.zeros(1, 4, dim), torch.empty(1, 4, dim, device="cuda")
+    q[:, :, 0] = query
+    rows.cache.attention(0, q.cuda(), i32([n - 1]), out)
+    torch.cuda.synchronize()
+    got, among = out[0].double().cpu().numpy(), rows.v[0][0][best]
+    tol = (n / 4 + 64) * 2.0 ** -23 * np.abs(among).max()
+    assert np.all(got >= among.min(0) - tol) and np.all(got <= among.max(0) + tol), query
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("n", [20, 32, 640, 650, 2570])
+@pytest.mark.parametrize("good, bad", [(-3.0, -5.0), (5.0, 3.0), (0.0, -3.0)])
+def test_scores_far_from_zero(dim, n, good, bad):
+    for query in (1e5, 1e8, 3e12, 1e20, 1e32, 1e36):
+        check_one_sided(dim, n, good, bad, query, n)
