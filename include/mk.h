@@ -379,7 +379,7 @@ mk_status mk_qcache_reorder(const mk_qcache* c, int rows, const int32_t* parents
  * Both products are exact sums of whole numbers (a head's queries in 30 bits of its largest, the softmax's
  * weights times their block's value scale in 31 bits of the largest so far), scaled and added in fp32; the
  * softmax's sum is fp32 and takes every key at its weight, whatever the sizes of the values. The open block is fp32. A query
- * head with an infinity or a NaN gives NaN. One or two kernel launches; no allocation,
+ * head with an infinity or a NaN gives NaN, as does a q . k beyond fp32's range. One or two kernel launches; no allocation,
  * capturable; the same inputs give the same bits. */
 mk_status mk_qcache_attention(const mk_qcache* c, int layer, int rows, int n_heads, int max_ctx, const float* q,
                               const int32_t* positions, float* out, void* workspace, size_t workspace_bytes,

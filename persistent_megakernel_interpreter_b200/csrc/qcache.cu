@@ -344,7 +344,7 @@ __device__ __forceinline__ void attn_blocks(const AttnArgs& a, AttnSmem<HD>& sm,
 #pragma unroll
         for (int e = 0; e < HD / 4; ++e) {
             big = fmaxf(big, fabsf(q[e]));
-            bad |= !(fabsf(q[e]) <= 3.4e38f);
+            bad |= !(fabsf(q[e]) < INFINITY);
         }
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));

@@ -199,3 +199,11 @@ def check_one_sided(dim, n, good, bad, query, seed):
 def test_scores_far_from_zero(dim, n, good, bad):
     for query in (1e5, 1e8, 3e12, 1e20, 1e32, 1e36):
         check_one_sided(dim, n, good, bad, query, n)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("n", [20, 32, 640, 650, 2570])
+def test_queries_of_the_largest_number(dim, n):
+    """Any finite query counts: scores of 1e35 here."""
+    for sign in (1.0, -1.0):
+        check_one_sided(dim, n, sign * 2.0 ** -8, 0.0, sign * torch.finfo(torch.float32).max, n)
