@@ -276,8 +276,8 @@ mk_status mk_greedy_select(const float* logits, int batch, int vocab, int32_t* n
  *   positions     device int32 [batch * beams] or NULL: each is incremented by one
  * A masked logit (-infinity) and a NaN are chosen only where nothing else is left, with score
  * -infinity; they add nothing to the row's sum. Infinite logits share their row's probability.
- * next_scores may be scores, and next_finished may be finished (with n_out == beams); any other
- * overlap of inputs and outputs is an error that is not detected.
+ * next_scores may be scores, and next_finished may be finished: of several sequences only with n_out ==
+ * beams (else MK_ERR_INVALID_ARG). Any other overlap of inputs and outputs is an error that is not detected.
  * Enqueues one kernel launch (one cluster of CTAs per sequence) on the calling thread's current
  * device, which must own the buffers and the stream; no synchronisation, no allocation, no
  * workspace, capturable in a CUDA graph. MK_ERR_INVALID_ARG for a NULL required pointer, a size

@@ -507,6 +507,8 @@ static mk_status beam_select(const float* logits, int64_t row_stride, int batch,
     if ((int64_t)beams * vocab < n_out) return MK_ERR_INVALID_ARG;
     if (finished && (eos < 0 || eos >= vocab)) return MK_ERR_INVALID_ARG;
     if (next_finished && !finished) return MK_ERR_INVALID_ARG;
+    // in place, a sequence's results may not lie where another's are still read
+    if (batch > 1 && n_out != beams && (next_scores == scores || (finished && next_finished == finished))) return MK_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(logits) & 3) return MK_ERR_INVALID_ARG;
     mk::BeamArgs a{};
     a.logits = logits;

@@ -271,7 +271,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, next_tokens: torch.T
     log_softmax(logits). A beam with a nonzero ``finished`` (int32 [sequences][beams]) goes on with
     ``eos`` at its own score; ``next_finished`` receives who is finished then. ``positions``
     (optional, one per row) are advanced by one. ``next_scores`` may be ``scores`` and
-    ``next_finished`` may be ``finished``. ``status`` (int32 [1], optional): the status of the step that the
+    ``next_finished`` may be ``finished`` (where n_out is beams, or there is one sequence). ``status`` (int32 [1], optional): the status of the step that the
     logits come from; where it is not 0 nothing is chosen: the parents are -1 and all else stays as it is."""
     _lib.check(_lib.call().beam_select(logits, scores, next_tokens, parents, next_scores, finished, eos, next_finished,
                                        positions, stream, status), "mk_beam_select")

@@ -43,3 +43,18 @@ def test_infinite_logits_beside_the_largest_number(batch, beams, vocab):
     x[:, 1] = -np.inf                                        # and without infinities
     x[np.isposinf(x)] = BIG
     check(x, scores, min(8, vocab))
+
+
+@pytest.mark.parametrize("batch, beams, n_out", [(1, 6, 2), (1, 6, 6), (5, 3, 3)])
+def test_in_place_where_it_is_allowed(batch, beams, n_out):
+    g = np.random.default_rng(beams)
+    x, scores = g.standard_normal((batch * beams, 2000)).astype(np.float32), -g.random((batch, beams)).astype(np.float32)
+    fin = g.random((batch, beams)) < 0.3
+    tok, par, tot, nf = select(x, scores, n_out, fin, 9)
+    sc, f = torch.from_numpy(scores).cuda(), torch.from_numpy(fin.astype(np.int32)).cuda()
+    t, p = (torch.zeros(batch, n_out, dtype=torch.int32, device="cuda") for _ in range(2))
+    beam_select(torch.from_numpy(x).cuda(), sc, t, p, sc, finished=f, eos=9, next_finished=f)
+    torch.cuda.synchronize()
+    assert np.array_equal(t.cpu().numpy(), tok) and np.array_equal(p.cpu().numpy(), par)
+    assert np.array_equal(f.view(-1)[:batch * n_out].cpu().numpy().reshape(batch, n_out), nf)
+    assert np.allclose(sc.view(-1)[:batch * n_out].cpu().numpy().reshape(batch, n_out), tot, rtol=2e-6, atol=1e-5)

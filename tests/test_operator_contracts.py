@@ -57,3 +57,13 @@ def test_a_cache_on_another_device_than_the_model_is_refused(monkeypatch):
     cache._device = 0
     with pytest.raises(RuntimeError, match="reached"):
         mk.decode_step_qcache_workspace(cache, 1, 64)
+
+
+@pytest.mark.parametrize("batch, beams, n_out, scores, finished, code", [
+    (2, 4, 2, True, False, INVALID), (2, 4, 8, True, False, INVALID), (2, 4, 2, False, True, INVALID), (3, 2, 1, True, True, INVALID)])
+def test_a_selection_in_place_refuses_where_sequences_would_overlap(batch, beams, n_out, scores, finished, code):
+    """Sequence b's results at b * n_out would lie among the scores of another, which may still be read."""
+    other = ctypes.c_void_p(1 << 20)
+    got = _lib.lib().mk_beam_select(PTR, 100, batch, beams, 100, n_out, PTR, PTR, 5, other, other, PTR if scores else other,
+                                    PTR if finished else other, None, None)
+    assert got == code
