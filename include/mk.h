@@ -311,7 +311,7 @@ mk_status mk_beam_select_checked(const float* logits, int64_t row_stride, int ba
  *                    its parent (a shared prompt) and are not moved
  * Slots outside those ranges and rows >= rows are not touched. Enqueues one kernel launch on the
  * calling thread's current device; no synchronisation, no allocation, capturable. MK_ERR_INVALID_ARG
- * for a NULL pointer, an unaligned cache or a bad row count, MK_ERR_UNSUPPORTED for a geometry
+ * for a NULL pointer, an unaligned cache, caches that overlap or a bad row count, MK_ERR_UNSUPPORTED for a geometry
  * outside mk_create's ranges. */
 mk_status mk_cache_reorder(const mk_config* cfg, void* k_cache, void* v_cache, int rows, const int32_t* parents,
                            const int32_t* lengths, const int32_t* starts, void* stream);

@@ -193,7 +193,11 @@ extern "C" mk_status mk_cache_reorder(const mk_config* cfg, void* k_cache, void*
         cfg->max_batch < 1 || cfg->max_batch > mk::kMaxBatch)
         return MK_ERR_UNSUPPORTED;
     if (rows < 1 || rows > cfg->max_batch) return MK_ERR_INVALID_ARG;
-    if ((reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache)) & 15) return MK_ERR_INVALID_ARG;
+    const uintptr_t k = reinterpret_cast<uintptr_t>(k_cache), v = reinterpret_cast<uintptr_t>(v_cache);
+    if ((k | v) & 15) return MK_ERR_INVALID_ARG;
+    // both are moved at once: a column may belong to one of them only
+    const size_t bytes = (size_t)cfg->n_layers * cfg->max_batch * cfg->n_kv_heads * cfg->max_seq * cfg->head_dim * 2;
+    if ((k < v ? v - k : k - v) < bytes) return MK_ERR_INVALID_ARG;
     mk::MoveArgs a{};
     const uint32_t sb = 2u * (uint32_t)cfg->head_dim;
     a.t[0] = {static_cast<uint8_t*>(k_cache), sb, (uint32_t)cfg->max_seq, mk::kSpanAll};

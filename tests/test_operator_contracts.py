@@ -67,3 +67,12 @@ def test_a_selection_in_place_refuses_where_sequences_would_overlap(batch, beams
     got = _lib.lib().mk_beam_select(PTR, 100, batch, beams, 100, n_out, PTR, PTR, 5, other, other, PTR if scores else other,
                                     PTR if finished else other, None, None)
     assert got == code
+
+
+@pytest.mark.parametrize("apart, code", [(0, INVALID), (16, INVALID), (-16, INVALID), (131056, INVALID), (-131056, INVALID)])
+def test_reorder_refuses_caches_that_overlap(apart, code):
+    """Keys and values are moved by the same launch: where they overlap, a slot would be read and written by two threads.
+    One cache here is 2 x 4 x 2 x 64 x 64 elements, 131072 bytes."""
+    cfg = _lib.MkConfig(2, 0, 0, 2, 64, 0, 0, 0.0, 0.0, 4, 64)
+    at = 1 << 20
+    assert _lib.lib().mk_cache_reorder(ctypes.byref(cfg), at, at + apart, 2, PTR, PTR, None, None) == code
