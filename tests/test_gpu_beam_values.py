@@ -58,3 +58,29 @@ def test_in_place_where_it_is_allowed(batch, beams, n_out):
     assert np.array_equal(t.cpu().numpy(), tok) and np.array_equal(p.cpu().numpy(), par)
     assert np.array_equal(f.view(-1)[:batch * n_out].cpu().numpy().reshape(batch, n_out), nf)
     assert np.allclose(sc.view(-1)[:batch * n_out].cpu().numpy().reshape(batch, n_out), tot, rtol=2e-6, atol=1e-5)
+
+
+# pieces of a row and threads that take a piece's tokens in turn, by the launch's rule
+CUTS = [(1, 1, 128256, 8, 256), (2, 4, 128256, 4, 512), (1, 1, 49000, 8, 128), (5, 8, 20000, 1, 512)]
+
+
+@pytest.mark.parametrize("batch, beams, vocab, pieces, threads", CUTS)
+@pytest.mark.parametrize("n_out, share", [(32, 30 / 128), (8, 7 / 32)])
+def test_more_above_the_bound_than_the_list_holds(batch, beams, vocab, pieces, threads, n_out, share):
+    """Everything that is large sits with a few of a piece's threads, fewer than n_out of the groups whose maxima give the bound:
+    the bound is one of the small numbers, thousands lie above it, and it has to be raised."""
+    g = np.random.default_rng(vocab + n_out)
+    size = -(-vocab // pieces)
+    hot = np.arange(vocab) % size % threads < int(share * threads)
+    x = g.standard_normal((batch * beams, vocab)).astype(np.float32)
+    scores = -g.random((batch, beams)).astype(np.float32)
+    x[:, hot] += 100.0
+    check(x, scores, n_out)                                  # all of them different
+    x[:, hot] = np.sort(x[:, hot], axis=1)
+    check(x, scores, n_out)                                  # in order: the largest at the end
+    x[:, hot] = 77.0 + (np.arange(hot.sum()) % 2).astype(np.float32)
+    check(x, scores, n_out)                                  # half of them the largest
+    x[:, hot] = 77.0 + (np.arange(hot.sum()) % 500 == 3).astype(np.float32)
+    check(x, scores, n_out)                                  # a few the largest, the others equal
+    x[:, hot] = 77.0 + np.minimum(np.arange(hot.sum()), 40).astype(np.float32)
+    check(x, scores, n_out)
