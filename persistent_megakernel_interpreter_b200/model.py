@@ -200,8 +200,8 @@ class Megakernel:
                                         stream=s)
             else:
                 self.decode_step(tokens, positions, cache[0], cache[1], logits, stream=s)
-            beam_select(chosen_from, scores, tokens.view_as(scores), to.view_as(scores), scores,
-                        finished=finished, eos=eos, next_finished=finished, positions=positions, stream=s, status=status)
+            _lib.check(_lib.call().beam_select(chosen_from, scores, tokens.view_as(scores), to.view_as(scores), scores, finished,
+                                               eos, finished, positions, s, status), "mk_beam_select")
             if isinstance(cache, QCache):
                 cache.reorder(to, positions, starts=starts, stream=s)
             else:
@@ -273,6 +273,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, next_tokens: torch.T
     (optional, one per row) are advanced by one. ``next_scores`` may be ``scores`` and
     ``next_finished`` may be ``finished`` (where n_out is beams, or there is one sequence). ``status`` (int32 [1], optional): the status of the step that the
     logits come from; where it is not 0 nothing is chosen: the parents are -1 and all else stays as it is."""
+    assert status is None or isinstance(status, torch.Tensor), "status: a tensor is wanted"  # the binding takes addresses too
     _lib.check(_lib.call().beam_select(logits, scores, next_tokens, parents, next_scores, finished, eos, next_finished,
                                        positions, stream, status), "mk_beam_select")
 

@@ -76,3 +76,13 @@ def test_reorder_refuses_caches_that_overlap(apart, code):
     cfg = _lib.MkConfig(2, 0, 0, 2, 64, 0, 0, 0.0, 0.0, 4, 64)
     at = 1 << 20
     assert _lib.lib().mk_cache_reorder(ctypes.byref(cfg), at, at + apart, 2, PTR, PTR, None, None) == code
+
+
+def test_a_status_that_is_no_tensor_is_refused():
+    """A number would be taken for a device address."""
+    import torch
+    from persistent_megakernel_interpreter_b200.model import beam_select
+    x, s, t = torch.zeros(2, 8), torch.zeros(1, 2), torch.zeros(1, 2, dtype=torch.int32)
+    for bad in (1, 0, 4096, True):
+        with pytest.raises(AssertionError, match="status"):
+            beam_select(x, s, t, t, s, status=bad)
