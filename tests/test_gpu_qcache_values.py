@@ -207,3 +207,27 @@ def test_queries_of_the_largest_number(dim, n):
     """Any finite query counts: scores of 1e35 here."""
     for sign in (1.0, -1.0):
         check_one_sided(dim, n, sign * 2.0 ** -8, 0.0, sign * torch.finfo(torch.float32).max, n)
+
+
+@pytest.mark.parametrize("max_ctx", [900, 2000])
+def test_prefixes_captured_and_replayed_with_other_lengths(max_ctx):
+    g = np.random.default_rng(max_ctx)
+    k, v = (normal(g, 2, 2, 2000, 64).bfloat16() for _ in range(2))
+    rows = Rows(k, v, [2000, 1500])
+    q = normal(g, 2, 8, 64)
+    qd, out = q.cuda(), torch.zeros(2, 8, 64, device="cuda")
+    pos, lengths, ws = i32([0, 0]), i32([2000, 1500]), rows.cache.attention_workspace(2, 8, max_ctx)
+    rows.cache.attention(0, qd, pos, out, max_ctx=max_ctx, workspace=ws, lengths=lengths)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rows.cache.attention(0, qd, pos, out, max_ctx=max_ctx, workspace=ws, lengths=lengths)
+    for at in ([1999, 1499], [40, 1000], [-1, 70], [899, 3]):
+        pos.copy_(i32(at))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        rows.check(q, at, max_ctx, keys=[min(p + 1, max_ctx) for p in at], lengths=lengths)
+        rows.cache.attention(0, qd, pos, out, max_ctx=max_ctx, workspace=ws, lengths=lengths)
+        torch.cuda.synchronize()
+        assert torch.equal(got, out)
