@@ -261,7 +261,7 @@ mk_status mk_greedy_select(const float* logits, int batch, int vocab, int32_t* n
  * the lower token. Totals are formed and compared in 64 bits, from a row maximum and a
  * 32-bit sum; scores are rounded to fp32 on the way out.
  *   logits        device fp32 [batch * beams][vocab], rows row_stride elements apart
- *                 (row_stride >= vocab; any 4-byte alignment, 16-byte rows are faster)
+ *                 (row_stride >= vocab; any 4-byte alignment, all alike)
  *   beams         1..16; n_out 1..32 and at most beams * vocab; vocab 1..2^24
  *   scores        device fp32 [batch][beams], running log probabilities; a beam that
  *                 is not in use has -infinity

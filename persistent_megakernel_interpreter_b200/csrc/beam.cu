@@ -22,7 +22,7 @@
 // 32 x 8 rows of 50257 (38.6 MB) in 17 us. What bounds it is the chain, not the bytes: for 2 x 4 rows about
 // 1.0 us to the first load, 2.2 us of loads, 1.0 us to join the maxima, 1.2 us to gather, 0.3 us to rank, 0.8 us for the
 // cluster's barrier, 1.7 us for totals and merging. (Keeping the logits in registers for the gathering
-// spills: 10.2 and 20.5 us.)
+// spills: 10.2 and 20.5 us. As it is, the forms of 256 and 512 threads spill 8 bytes.)
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <math.h>

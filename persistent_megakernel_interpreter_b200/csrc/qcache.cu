@@ -40,7 +40,7 @@ __device__ __forceinline__ float bf(uint32_t bits16) { return __uint_as_float(bi
 // has read the tail's old tokens.
 //
 // Bound by HBM (2 bytes in, 1 out). Small CTAs at 64 registers a thread: 16 layers of four prompts of
-// up to 4001 tokens (688 MB) in 101 us, 104% of the measured copy rate (145 us with 8 warps a CTA, one warp a
+// up to 4001 tokens (688 MB) in 101 us in a graph, 104% of the measured copy rate, and 101 to 103 as calls (145 us with 8 warps a CTA, one warp a
 // block and 79 registers); one token of eight rows in 1.3 us.
 template <int HD>
 __global__ void __launch_bounds__(32 * kAppWarps, 8) k_append(const __grid_constant__ AppendArgs a) {
@@ -155,21 +155,25 @@ __global__ void __launch_bounds__(32 * kAppWarps, 8) k_append(const __grid_const
 // plus the sum (below 2^22 in magnitude: 128 * 127 * 128 in a score, 255 * 127 * 64 in
 // an output), and one FMA turns each into its share of the fp32 result.
 //
+// A score is rounded once to fp32 and is the same number in the maximum and in its weight, whatever its size.
+// Keys behind a cut inside a closed block get a score of -infinity.
+//
 // A warp works alone on a batch of 8 KB (64 keys and values of 64 dims, 32 of 128), with
 // a running (M, l, O) of its own, fed by a private ring of asynchronous copies; the warps
 // join at the end.
 //
-// Bound by HBM: 2 * dim bytes a key and KV head. Measured on one B200: 4 rows of up to 60001 keys of 128 dims
-// (308 MB) in 51.5 us, 5.97 TB/s (91% of the measured copy rate); 8 rows of up to 16384 keys of 64 dims (105 MB)
-// in 21.6 us (75%); 129 keys in 3.2 us. Around the stream of bytes there are about 5 us: 1.5 to launch, 0.7
-// for the plan, 1 until the first batch is here, 0.7 to join a CTA's warps, 1.5 for the joining kernel. As fp16
-// products (codes converted, the other operand in two parts) the same took 32 and 114 us at first and 30 and
-// 72 with the rings: twice the instructions for half the products.
+// Bound by HBM: 2 * dim bytes a key and KV head. Measured on one B200, in a graph (as calls in a stream): 4 rows of
+// up to 60001 keys of 128 dims (307 MB) in 50.8 us (52 to 54), 6.05 TB/s, 92% of the measured copy rate; 8 rows of up to
+// 16384 keys of 64 dims (105 MB) in 21.7 us (22.1), 74%; 129 keys in 3.2 us (3.4); one row of 16384 keys and 8 heads
+// in 7.9 us of 64 dims, 11.4 of 128. Around the stream of bytes there are about 5 us: 1.5 to launch, 0.7
+// for the plan, 1 until the first batch is here, 0.6 to join a CTA's warps, 1.5 for the joining kernel. As fp16
+// products (codes converted, the other operand in two parts) the two long ones took 32 and 114 us at first and 30
+// and 72 with the rings: twice the instructions for half the products.
 
 constexpr int kAttWarps = 4;
-// Batches in a warp's ring, and CTAs an SM holds. The 64-dim form needs about 180 registers a thread and
-// so runs two CTAs, with a batch more on the way each; at 128 dims three fit. 8 x 16384 keys of 64
-// dims: 23.8 us against 25.0 with (2, 3); 4 x 60001 of 128 dims: 56.4 us against 57.9 with (3, 2).
+// Batches in a warp's ring, and CTAs an SM holds: two of the 64-dim split's CTAs (253 registers a thread), with a batch
+// more on the way each; three at 128 dims (168 registers, 8 bytes of spills). 8 x 16384 keys of 64 dims: 21.7 us, 21.8 with
+// (2, 3); 4 x 60001 of 128 dims: 50.8 us, 53.1 with (3, 2).
 __host__ __device__ constexpr int attn_stages(int hd) { return hd == 64 ? 3 : 2; }
 __host__ __device__ constexpr int attn_per_sm(int hd) { return hd == 64 ? 2 : 3; }
 constexpr int kHalf = 4096;            // bytes of a batch's keys, and of its values
@@ -680,8 +684,8 @@ struct RowKeys {
 
 // The order in which the split deals out blocks: row by row, head by head, each (row, KV head) with its
 // blocks (the open one included) behind kPad units without work, which stand for what starting and
-// joining one more piece costs the CTA that has them. 4 / 8 / 12 / 16 / 24 units: 52.4 / 52.3 / 51.6 /
-// 51.7 / 51.7 us at 4 x 60001 keys of 128 dims, 22.0 / 21.7 / 21.9 / 21.6 / 21.5 at 8 x 16384 of 64.
+// joining one more piece costs the CTA that has them. 4 / 8 / 12 / 16 / 24 units: 52.3 / 52.0 / 51.9 /
+// 51.6 / 50.8 us at 4 x 60001 keys of 128 dims, 22.2 / 21.8 / 21.9 / 21.6 / 21.7 at 8 x 16384 of 64.
 constexpr int kPad = 24;
 __device__ __forceinline__ int attn_units(int keys) { return (keys + kQBlock - 1) / kQBlock; }
 __device__ __forceinline__ int attn_share(int keys) { return keys ? attn_units(keys) + kPad : 0; }
@@ -817,8 +821,8 @@ __global__ void __launch_bounds__(32 * kAttWarps, attn_per_sm(HD)) k_attn_split(
 }
 
 // Joins the partials of one (row, query head): warps take kJoinEach slots in turn, lanes the dims. (8, 8)
-// against (8, 4) warps and slots: 16.1 and 16.8 us for one row of 65536 keys and 8 heads of 64 dims, 9.1 and 11.5
-// with one head (444 partials); 16 warps are no faster there and 1 us slower at 8 x 8 pairs.
+// against (8, 4) warps and slots: 15.8 and 17.2 us for one row of 65536 keys and 8 heads of 64 dims, 8.7 and 10.7
+// with one head; 16 warps are no faster there and 1 us slower at 8 x 8 pairs.
 constexpr int kJoinWarps = 8, kJoinEach = 8;
 template <int HD>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_merge_q(const __grid_constant__ AttnArgs a) {
@@ -839,8 +843,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_merge_q(const __grid_c
     const int c0 = share ? P.owner(first + kPad) : 0, total = share ? P.owner(first + share - 1) - c0 + 1 : 0;
     cudaGridDependencySynchronize();
     // kJoinEach partials of a warp at once, every load issued before the first is used. At 128 dims lane k of every
-    // eight forms the factor of the k-th partial and shuffles pass it (2 rows of 4096 keys and 8 heads: 8.8 us, 9.0 where every
-    // lane forms all eight), at 64 dims every lane forms them (6.1 us, 6.3 with shuffles).
+    // eight forms the factor of the k-th partial and shuffles pass it (one row of 1024 keys and 8 heads: 5.6 us, 6.0 where
+    // every lane forms all eight), at 64 dims every lane forms them (2 rows of 16384 keys: 9.1 us, 9.8 with shuffles).
     float M = -INFINITY, l = 0.f, o[D];
 #pragma unroll
     for (int d = 0; d < D; ++d) o[d] = 0.f;
@@ -920,9 +924,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_merge_q(const __grid_c
 // ------------------------------------------------------------------ launches
 
 // One CTA per (row, KV head) up to these contexts, in one kernel; beyond, the split and its joining kernel.
-// With 8 pairs the two take 4.8 and 4.7 us at 1024 keys of 64 dims, 7.5 and 4.9 at 2048; 5.4 and 5.7 at 512 keys of
-// 128, 8.1 and 5.8 at 1024. With 64 pairs 7.6 and 8.0 us at 2048 keys of 64 dims, 12.9 and 9.7 at 4096;
-// 8.2 and 9.2 at 1024 of 128, 13.5 and 10.8 at 2048.
+// With 8 pairs the two take 4.7 and 4.6 us at 1024 keys of 64 dims, 7.4 and 4.8 at 2048; 5.3 and 5.4 at 512 keys of
+// 128, 8.1 and 5.4 at 1024. With 64 pairs 7.4 and 8.0 us at 2048 keys of 64 dims, 12.8 and 9.8 at 4096;
+// 8.2 and 9.1 at 1024 of 128, 13.7 and 10.8 at 2048.
 bool attn_is_split(int hd, int pairs, int max_ctx) { return max_ctx > (pairs >= 32 ? 131072 : 65536) / hd; }
 // Floats of the partials' maxima and sums; the outputs behind them are read 16 bytes at a time.
 size_t attn_ml_floats(size_t slots) { return (2 * slots + 3) / 4 * 4; }
